@@ -26,7 +26,8 @@ EXPORTS = ("lin_attn_chunk_fwd", "gdn_chunk_fwd", "lin_attn_chunk_fwd_varlen", "
            "lin_attn_chunk_fwd_ex", "gdn_chunk_fwd_ex", "gdn_decode_step", "gdn_decode_step_ex",
            "gdn_status_str", "gdn_sync_status", "gdn_set_wait_limit_for_testing", "gdn_version",
            "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_bytes", "gdn_chunk_bwd_noalloc", "gdn_state_compose",
-           "gdn_state_identity", "gdn_chunk_fwd_host", "gdn_chunk_fwd_host_staging_bytes")
+           "gdn_state_identity", "gdn_chunk_fwd_host", "gdn_chunk_fwd_host_staging_bytes", "gdn_plan_batch",
+           "gdn_kv_append", "gdn_kv_attn", "gdn_kv_attn_workspace_bytes", "gdn_decode_slots")
 
 
 GDN_XNORM = {None: 0, "rms": 1, "layer": 2}
@@ -81,6 +82,15 @@ def _load() -> ctypes.CDLL:
     lib.gdn_chunk_fwd_host.argtypes = [P, P, P, P, P, P, P, P, P, Z, I, I, I, I, I, I, F, I, I, P]
     lib.gdn_chunk_fwd_host.restype = ctypes.c_int
     lib.gdn_state_identity.restype = ctypes.c_int
+    LL = ctypes.c_longlong
+    lib.gdn_plan_batch.argtypes = [P, P, I, P, I, P, P, I, I, I, P, P, P, P, P, P, P]
+    lib.gdn_kv_append.argtypes = [P, P, LL, LL, P, P, P, P, P, I, I, I, I, I, I, P]
+    lib.gdn_kv_attn_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gdn_kv_attn_workspace_bytes.restype = Z
+    lib.gdn_kv_attn.argtypes = [P, LL, P, P, P, P, P, P, P, P, P, P, Z, I, I, I, I, I, I, I, I, I, I, F, I, I, P]
+    lib.gdn_decode_slots.argtypes = [P, P, P, LL, LL, LL, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P]
+    for f in (lib.gdn_plan_batch, lib.gdn_kv_append, lib.gdn_kv_attn, lib.gdn_decode_slots):
+        f.restype = ctypes.c_int
     for f in (lib.lin_attn_chunk_fwd, lib.gdn_chunk_fwd, lib.lin_attn_chunk_fwd_varlen,
               lib.gdn_chunk_fwd_varlen, lib.lin_attn_chunk_fwd_ex, lib.gdn_chunk_fwd_ex,
               lib.gdn_decode_step, lib.gdn_decode_step_ex, lib.gdn_sync_status, lib.gdn_version):

@@ -50,6 +50,17 @@ gdn_status_t check_prefill(const void *q, const void *k, const void *v, const fl
 }  // namespace
 
 namespace gdn {
+// Checks the options of a call and takes them over; false for one that is not valid.
+bool set_fwd_opts(const gdn_fwd_opts_t &opts, bool has_g, FwdOpts *oo) {
+    if (opts.out_dtype != GDN_F32 && opts.out_dtype != GDN_BF16) return false;
+    if (opts.g_per_key != 0 && opts.g_per_key != 1) return false;
+    if (!opt_aligned4(opts.d_skip)) return false;
+    if (!set_xnorm(opts, oo)) return false;
+    oo->bf16 = opts.out_dtype == GDN_BF16;
+    oo->dskip = opts.d_skip;
+    oo->gate_per_key = opts.g_per_key == 1 && has_g;
+    return true;
+}
 // The per-chunk prep kernel and the per-head chain kernel (tc_vg.cu), dense bf16 batches at
 // dk = dv = 128, C = 64, with a stream-ordered workspace: vector-valued gates (per_key), and
 // scalar gates for few heads with long sequences (tc_vg_takes_scalar), whose sequences are then

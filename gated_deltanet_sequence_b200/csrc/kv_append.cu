@@ -1,0 +1,281 @@
+// gdn_kv_append: new K and V rows into the paged 8-bit cache, one power-of-two scale for each
+// block of tokens and head.
+//
+//   scale = 2^e, the smallest with max |x| <= 448 * 2^e;   code = e4m3(x / scale)
+// The scale is a power of two because e4m3 is a float: its relative step does not depend on the
+// scale, so a finer scale would buy less than a binade of range, while with powers of two x /
+// scale and the rescaling of codes already there are exact (until they fall below the smallest
+// normal, 2^-6), and appending a prompt in pieces gives what appending it at once gives.
+//
+// The unit of work is a run: consecutive rows that go to consecutive cache rows of one block,
+// for one head of K or V. One pass: the run's values stay in registers between the maximum and
+// the codes. A block of 256 threads looks over R rows and takes the runs that start there: runs
+// that a warp holds in a few registers (decode: one row) go one to a warp, longer ones (prompts)
+// to the whole block. DRAM bytes bound it: rows in, codes out.
+#include "common.cuh"
+#include "tc_kernels.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kAppThreads = 256, kAppWarps = kAppThreads / 32;
+constexpr int kMaxRows = 64, kMaxBs = 128;
+constexpr int kMaskWords = (kMaxRows + kMaxBs + 31) / 32;
+constexpr int kScaleExpMin = -100;
+constexpr int kWarpSteps = 4;   // a warp's run: at most 4 chunks of 8 values a lane
+
+struct AppArgs {
+    const void *x[2];
+    long long stride[2];
+    uint8_t *cache[2];
+    float *scale[2];
+    const int *slot;
+    int T, H, bs_log2, num_blocks, R;
+};
+
+// 8 values (one chunk) of a row, as fp32
+template <typename IT> struct Chunk;
+template <> struct Chunk<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+
+// largest finite magnitude
+template <typename IT>
+__device__ __forceinline__ float chunk_max(const Chunk<IT> &c) {
+    float f[8], m = 0.f;
+    c.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = fabsf(f[i]);
+        m = x < __int_as_float(0x7f800000) ? fmaxf(m, x) : m;
+    }
+    return m;
+}
+
+// exponent of the smallest power of two s, >= 2^kScaleExpMin, with amax <= 448 s: amax = 1.f *
+// 2^(E - 127) and 448 = 1.75 * 2^8
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax > 0.f ? max(e, kScaleExpMin) : kScaleExpMin;
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// two fp32 -> two e4m3 (nearest even; beyond 448 to 448; NaN to NaN), lo in the low byte
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+template <typename IT>
+__device__ __forceinline__ void store_codes(uint8_t *dst, const Chunk<IT> &c, float inv) {
+    float f[8];
+    c.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = f[i] * inv;      // exact: inv is a power of two
+        // an infinity would be taken to 448: it is stored as NaN instead, so that it shows
+        f[i] = fabsf(f[i]) == __int_as_float(0x7f800000) ? __int_as_float(0x7fffffff) : x;
+    }
+    uint2 w;
+    w.x = to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16);
+    w.y = to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16);
+    *reinterpret_cast<uint2 *>(dst) = w;
+}
+
+// The scale of a run's block: fresh blocks take what the run needs, others the larger of that
+// and their own.
+__device__ __forceinline__ float run_scale(float amax, bool fresh, float old) {
+    const float fit = exp2i(scale_exp(amax));
+    return fresh || !(old >= fit) ? fit : old;
+}
+
+// Codes of the block's earlier rows, `bytes` of them, times ratio (a power of two below 1);
+// threads t of nt.
+__device__ __forceinline__ void rescale_codes(uint8_t *p, int bytes, float ratio, int t, int nt) {
+    for (int i = t * 8; i < bytes; i += nt * 8) {
+        uint2 w = *reinterpret_cast<const uint2 *>(p + i);
+        uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 a = from_e4m3x2(u[j] & 0xffffu), b = from_e4m3x2(u[j] >> 16);
+            u[j] = to_e4m3x2(a.x * ratio, a.y * ratio) | (to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+        }
+        *reinterpret_cast<uint2 *>(p + i) = make_uint2(u[0], u[1]);
+    }
+}
+
+template <int D, typename IT>
+__global__ void __launch_bounds__(kAppThreads)
+kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
+    constexpr int CPR = D / 8;                           // chunks a row
+    constexpr int STEPS = kMaxBs * CPR / kAppThreads;    // chunks a thread of a block's longest run
+    __shared__ int s_slot[kMaxRows + kMaxBs];
+    __shared__ uint32_t s_brk[kMaskWords];
+    __shared__ int s_long[kMaxRows], s_short[kMaxRows], s_nlong, s_nshort;
+    __shared__ float s_max[kAppWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.y, z = blockIdx.z, bs = 1 << a.bs_log2;
+    const long long r0 = static_cast<long long>(blockIdx.x) * a.R;
+    const int nslots = a.num_blocks << a.bs_log2;
+    const IT *x = static_cast<const IT *>(z ? a.x[1] : a.x[0]) + h * D;
+    const long long stride = z ? a.stride[1] : a.stride[0];
+    uint8_t *cache = z ? a.cache[1] : a.cache[0];
+    float *scale = z ? a.scale[1] : a.scale[0];
+
+    // slots of this block's rows and of the rows a run may reach past them; a bit where a run starts
+    // (or a row that is skipped, or the end)
+    const int span = a.R + bs;
+    if (tid == 0) s_nlong = s_nshort = 0;
+    for (int base = 0; base < ((span + 31) & ~31); base += kAppThreads) {
+        const int i = base + tid;
+        const long long r = r0 + i;
+        int s = -1, prev = -1;
+        if (i < span && r < a.T) {
+            s = a.slot[r];
+            if (r > 0) prev = a.slot[r - 1];
+            if (s < -1 || s >= nslots) {
+                if (i < a.R && h == 0 && z == 0) atomicOr(err, kErrBadSeqlens);
+                s = -1;
+            }
+        }
+        const bool starts = s < 0 || prev < 0 || s != prev + 1 || (s & (bs - 1)) == 0 || r == 0;
+        if (i < span) s_slot[i] = s;
+        const unsigned bits = __ballot_sync(0xffffffffu, starts);
+        if (lane == 0 && (base >> 5) + warp < kMaskWords) s_brk[(base >> 5) + warp] = bits;
+    }
+    __syncthreads();
+    if (tid < a.R && s_slot[tid] >= 0 && ((s_brk[tid >> 5] >> (tid & 31)) & 1u)) {
+        // rows to the next start: at most bs, since a block's first row starts a run
+        int w = tid >> 5;
+        uint32_t m = (tid & 31) == 31 ? 0u : s_brk[w] & (0xfffffffeu << (tid & 31));
+        while (m == 0 && 32 * (w + 1) < span) m = s_brk[++w];
+        const int end = m ? min(32 * w + __ffs(m) - 1, span) : span;
+        const int len = end - tid;
+        const int id = tid | (len << 8);
+        if (len * CPR <= 32 * kWarpSteps) s_short[atomicAdd(&s_nshort, 1)] = id;
+        else s_long[atomicAdd(&s_nlong, 1)] = id;
+    }
+    __syncthreads();
+
+    // ---- long runs: the whole block
+    const int nlong = s_nlong, nshort = s_nshort;
+    for (int e = 0; e < nlong; ++e) {
+        const int i0 = s_long[e] & 255, len = s_long[e] >> 8;
+        const int slot = s_slot[i0], off = slot & (bs - 1);
+        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h;
+        const float old = scale[bh];
+        Chunk<IT> c[STEPS];
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+            const int id = tid + j * kAppThreads;
+            if (id < len * CPR) c[j].load(x + (r0 + i0 + id / CPR) * stride + (id % CPR) * 8);
+            else c[j].zero();
+        }
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) m = fmaxf(m, chunk_max(c[j]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) s_max[warp] = m;
+        __syncthreads();
+        m = s_max[0];
+#pragma unroll
+        for (int w = 1; w < kAppWarps; ++w) m = fmaxf(m, s_max[w]);
+        const float sc = run_scale(m, off == 0, old);
+        const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
+        uint8_t *dst = cache + (bh << a.bs_log2) * D;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+            const int id = tid + j * kAppThreads;
+            if (id < len * CPR) store_codes(dst + off * D + id * 8, c[j], inv);
+        }
+        if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, tid, kAppThreads);
+        __syncthreads();      // everyone has read the old scale and s_max
+        if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
+    }
+
+    // ---- short runs: one to a warp
+    for (int e = warp; e < nshort; e += kAppWarps) {
+        const int i0 = s_short[e] & 255, len = s_short[e] >> 8;
+        const int slot = s_slot[i0], off = slot & (bs - 1);
+        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h;
+        const float old = off > 0 ? scale[bh] : 0.f;
+        Chunk<IT> c[kWarpSteps];
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < kWarpSteps; ++j) {
+            const int id = lane + j * 32;
+            if (id < len * CPR) c[j].load(x + (r0 + i0 + id / CPR) * stride + (id % CPR) * 8);
+            else c[j].zero();
+        }
+#pragma unroll
+        for (int j = 0; j < kWarpSteps; ++j) m = fmaxf(m, chunk_max(c[j]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float sc = run_scale(m, off == 0, old);
+        const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
+        uint8_t *dst = cache + (bh << a.bs_log2) * D;
+#pragma unroll
+        for (int j = 0; j < kWarpSteps; ++j) {
+            const int id = lane + j * 32;
+            if (id < len * CPR) store_codes(dst + off * D + id * 8, c[j], inv);
+        }
+        if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, lane, 32);
+        __syncwarp();
+        if (lane == 0 && (off == 0 || sc != old)) scale[bh] = sc;
+    }
+}
+
+}  // namespace
+
+gdn_status_t launch_kv_append(const void *k, const void *v, long long ks, long long vs, const int *slot, void *kc,
+                              void *vc, float *ksc, float *vsc, int T, int H, int d, int num_blocks, int block_size,
+                              gdn_dtype_t in_dtype, cudaStream_t stream) {
+    unsigned *err = device_error_word();
+    if (!err) return GDN_ERR_CUDA;
+    int lg = 0;
+    while ((1 << lg) < block_size) ++lg;
+    AppArgs a{{k, v}, {ks, vs}, {static_cast<uint8_t *>(kc), static_cast<uint8_t *>(vc)}, {ksc, vsc}, slot, T, H, lg,
+              num_blocks, 0};
+    a.R = T >= 4096 ? kMaxRows : kAppWarps;
+    const dim3 grid(static_cast<unsigned>((T + a.R - 1) / a.R), static_cast<unsigned>(H), 2);
+    if (in_dtype == GDN_F32) {
+        if (d == 128) kv_append_kernel<128, float><<<grid, kAppThreads, 0, stream>>>(a, err);
+        else kv_append_kernel<64, float><<<grid, kAppThreads, 0, stream>>>(a, err);
+    } else {
+        if (d == 128) kv_append_kernel<128, __nv_bfloat16><<<grid, kAppThreads, 0, stream>>>(a, err);
+        else kv_append_kernel<64, __nv_bfloat16><<<grid, kAppThreads, 0, stream>>>(a, err);
+    }
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace gdn

@@ -1,0 +1,671 @@
+// gdn_kv_attn, few rows a request (decode, drafted tokens): softmax attention over the paged
+// 8-bit cache, bound by the cache's bytes.
+//
+// Rows: the query tokens of a request times the query heads that share a KV head, 16 to a tile
+// (row R is token R / G, head R % G). A unit of work is (request, KV head, row tile); its cost is
+// its kv tiles of 128 tokens. All units' tiles form one line, cut into equal shares, one a block
+// (each block finds its share from the lengths, on the device): a long context is spread over
+// many blocks and short ones share one, whatever the mix, with nothing planned on the host. A unit
+// cut by a share's end leaves a partial (m, l, O) in the workspace, and kv_attn_join_kernel adds
+// the parts of each cut unit in order.
+//
+// Inside a block each of the four warps runs its own stream of 32-token steps with its own online
+// softmax: K and V codes come by TMA into the warp's ring (one lane issues, nobody else is waited
+// for), go to fp16 in registers (e4m3 fits fp16 exactly) and enter mma.m16n8k16 as the B operand,
+// queries and weights as A. The block scale, a power of two, multiplies the scores in fp32; V's is
+// carried as the unit of the accumulators (O is kept in units of the current block's V scale and
+// multiplied by the ratio, exactly, when it changes), so no operand is rounded for it. Queries are
+// divided by a power of two for each row so that fp16 holds them: bf16 ones enter exactly, fp32
+// ones as a sum of two fp16 parts, and the weights as two parts too where the output is fp32.
+//
+// The contraction index of an MMA may be permuted as long as both operands agree: a lane's
+// 16-byte load of 16 key coordinates feeds four k-steps, and V's token pairs come from two rows'
+// words by byte permutes. Rows of the 128-byte-swizzled tiles are taken in an order in which the
+// eight lanes of a quarter-warp hit different banks.
+#include <algorithm>
+
+#include "kv_attn.cuh"
+
+namespace gdn {
+namespace {
+using namespace ptx;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStep = 32;                   // tokens of a warp's step
+constexpr int kTile = kStep * kWarps;       // tokens of a block's tile
+constexpr int kRows = 16;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int D> struct Smem {
+    static constexpr int kBlocks = D == 128 ? 2 : 3;         // blocks an SM holds (registers)
+    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr int kStepBytes = kStep * D;             // K or V codes of a step
+    static constexpr int kStageBytes = 2 * kStepBytes;
+    static constexpr int kRing = kStages * kStageBytes;      // per warp
+    static constexpr int kMergeRow = D + 4;                  // floats; rows of the cross-warp merge, over the rings
+    static constexpr int kMerge = kWarps * kRows * kMergeRow * 4;
+    static constexpr int kData = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
+    static constexpr int kBytes = kData + 1024;              // slack to align to 1024
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four e4m3 codes -> two fp16 pairs (exact)
+__device__ __forceinline__ void e4m3_to_h2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+// Wait for phase `parity`, at most about `limit` cycles. The first look does not suspend the thread, so that a
+// limit shorter than the hardware's own suspension is kept too.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, long long limit) {
+    const uint32_t b = smem_u32(bar);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const long long t0 = clock64();
+    do {
+        if (clock64() - t0 > limit) return false;
+    } while (!mbar_try_wait(b, parity));
+    return true;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// x as two fp16 parts: hi + lo = x to 22 bits (|x| within fp16's normal range)
+__device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = pack_h2(x - f.x, y - f.y);
+}
+__device__ __forceinline__ uint32_t nan_halves(uint32_t h) {      // 0xffff in the halves that are NaN
+    const __half2 x = *reinterpret_cast<const __half2 *>(&h);
+    return __hneu2_mask(x, x);
+}
+
+// A block's row state while a unit runs, and the loop over its steps.
+template <int D, bool QSPLIT, bool PSPLIT>
+struct Worker {
+    static constexpr int KS = D / 16;          // k-steps of Q K^T
+    static constexpr int NT = D / 8;           // n-tiles of P V
+    uint32_t qa[KS][4], ql[QSPLIT ? KS : 1][4];
+    float o[NT][4];
+    float m[2], l[2], rf[2];                   // rows g and g + 8: maximum, this lane's part of the sum, score factor
+    int hi[2], lo[2];                          // positions a row sees: lo .. hi
+    float vu;                                  // V scale that the accumulators are in units of (0: none yet)
+
+    __device__ __forceinline__ static int token_of(int n) { return D == 128 ? (n & 1) * 4 + (n >> 1) : n; }
+
+    // one step: 32 tokens from position t0; sk, sv: shared addresses of the codes; ks, vs: the scales of the
+    // step's two halves; tok: tokens that exist (bit i: t0 + i); edge: some row does not see some token
+    __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[2], const float (&vs)[2],
+                                         uint32_t tok, bool edge) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        float s[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + token_of(g);
+            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                const int swz = D == 128 ? (r & 7) : ((r >> 1) & 3);
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(sk + r * D + (((c + 4 * half) ^ swz) << 4)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t b0, b1;
+                    e4m3_to_h2(w[i], b0, b1);
+                    mma16816(s[j], qa[4 * half + i], b0, b1);
+                    if (QSPLIT) mma16816(s[j], ql[4 * half + i], b0, b1);
+                }
+            }
+        }
+        // scores in base-2 exponents; c0, c1: row g, tokens token_of(2c), token_of(2c + 1); c2, c3: row g + 8
+        float mx[2] = {kNegInf, kNegInf};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = s[j][i] * (rf[i >> 1] * ks[j >> 1]);
+                if (edge) {
+                    const int t = 8 * j + token_of(2 * c + (i & 1));
+                    const bool see = ((tok >> t) & 1u) && t0 + t <= hi[i >> 1] && t0 + t >= lo[i >> 1];
+                    x = see ? x : kNegInf;
+                }
+                s[j][i] = x;
+                mx[i >> 1] = fmaxf(mx[i >> 1], x);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        }
+        float fac[2], base[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float mn = fmaxf(m[r], mx[r]);
+            base[r] = mn == kNegInf ? 0.f : mn;
+            fac[r] = ex2(m[r] - base[r]);
+            m[r] = mn;
+            l[r] *= fac[r];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[j][i] = ex2(s[j][i] - base[i >> 1]);
+                l[i >> 1] += s[j][i];
+            }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
+            const float u = vu == 0.f ? 1.f : vu / vs[hf];
+            vu = vs[hf];
+            const float f0 = (hf == 0 ? fac[0] : 1.f) * u, f1 = (hf == 0 ? fac[1] : 1.f) * u;
+            if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    o[i][0] *= f0; o[i][1] *= f0; o[i][2] *= f1; o[i][3] *= f1;
+                }
+            }
+            uint32_t p[4], pl[4];
+            float(&x)[4] = s[2 * hf], (&y)[4] = s[2 * hf + 1];
+            if (PSPLIT) {
+                split_h2(x[0], x[1], p[0], pl[0]);
+                split_h2(x[2], x[3], p[1], pl[1]);
+                split_h2(y[0], y[1], p[2], pl[2]);
+                split_h2(y[2], y[3], p[3], pl[3]);
+            } else {
+                p[0] = pack_h2(x[0], x[1]); p[1] = pack_h2(x[2], x[3]);
+                p[2] = pack_h2(y[0], y[1]); p[3] = pack_h2(y[2], y[3]);
+            }
+            // this lane's four V rows of the half: k = 2c, 2c + 1, 2c + 8, 2c + 9
+            const int ra = 16 * hf + token_of(2 * c), rb = 16 * hf + token_of(2 * c + 1);
+            constexpr int W = D / 32;           // words a lane takes of a row
+            uint32_t v[4][W];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (i & 1 ? rb : ra) + (i >> 1) * 8;
+                if constexpr (D == 128) {
+                    const int ch = (g & 1) * 4 + (g >> 1);
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                                 : "r"(sv + r * D + ((ch ^ (r & 7)) << 4)));
+                } else {
+                    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                                 : "=r"(v[i][0]), "=r"(v[i][1])
+                                 : "r"(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
+                }
+            }
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            bool nans = false;
+            if (edge) {        // rows that do not exist hold anything: their values are taken out
+                keep0 = (((tok >> ra) & 1u) ? 0xffffu : 0u) | (((tok >> rb) & 1u) ? 0xffff0000u : 0u);
+                keep1 = (((tok >> (ra + 8)) & 1u) ? 0xffffu : 0u) | (((tok >> (rb + 8)) & 1u) ? 0xffff0000u : 0u);
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t z = (v[i][w] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;      // a zero byte is a NaN code
+                        any |= ((z - 0x01010101u) & ~z & 0x80808080u) != 0u;
+                    }
+                nans = __any_sync(0xffffffffu, any);
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t e[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e4m3_to_h2(v[i][w], e[i][0], e[i][1]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t b0 = __byte_perm(e[0][q >> 1], e[1][q >> 1], q & 1 ? 0x7632 : 0x5410);
+                    uint32_t b1 = __byte_perm(e[2][q >> 1], e[3][q >> 1], q & 1 ? 0x7632 : 0x5410);
+                    float(&acc)[4] = o[4 * w + q];
+                    if (edge) {
+                        b0 &= keep0;
+                        b1 &= keep1;
+                        if (nans) {
+                            // a NaN among values that some row does not see: it must reach the rows that do, and
+                            // 0 * NaN must not reach the others. The rows it reaches are those with a 1 (a token
+                            // seen) against a 1 (a NaN there).
+                            const uint32_t n0 = nan_halves(b0), n1 = nan_halves(b1);
+                            b0 &= ~n0;
+                            b1 &= ~n1;
+                            uint32_t seen[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                uint32_t bits = 0u;
+#pragma unroll
+                                for (int e2 = 0; e2 < 2; ++e2) {
+                                    const int t = 16 * hf + 8 * (r >> 1) + token_of(2 * c + e2);
+                                    const bool see = ((tok >> t) & 1u) && t0 + t <= hi[r & 1] && t0 + t >= lo[r & 1];
+                                    if (see) bits |= 0x3c00u << (16 * e2);
+                                }
+                                seen[r] = bits;
+                            }
+                            float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma16816(hit, seen, n0 & 0x3c003c00u, n1 & 0x3c003c00u);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[r] = hit[r] > 0.f ? __int_as_float(0x7fffffff) : acc[r];
+                        }
+                    }
+                    mma16816(acc, p, b0, b1);
+                    if (PSPLIT) mma16816(acc, pl, b0, b1);
+                }
+            }
+        }
+    }
+};
+
+template <int D, bool QSPLIT, bool PSPLIT, typename IT>
+__global__ void __launch_bounds__(kThreads, Smem<D>::kBlocks)
+kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+    using S = Smem<D>;
+    using W = Worker<D, QSPLIT, PSPLIT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t s_bar[kWarps][S::kStages];
+    __shared__ Share s_share;
+    __shared__ float s_ml[kWarps][kRows][2];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int G = a.Hq / a.Hkv;
+
+    cudaTriggerProgrammaticLaunchCompletion();     // the join kernel's blocks may take their places; they wait there
+    if (lane == 0) {
+        for (int i = 0; i < S::kStages; ++i) mbar_init(&s_bar[warp][i], 1);
+        fence_mbar_init();
+    }
+    find_share<kThreads>(a, blockIdx.x, gridDim.x, &s_share);      // ends with a block barrier
+    const Share sh = s_share;
+    CutUnit cut{};
+    if (sh.begin >= sh.end) {
+        if (tid == 0) a.cuts[blockIdx.x] = cut;
+        return;
+    }
+    const uint32_t ring = smem_u32(smem) + warp * S::kRing;
+    uint32_t phase = 0;                     // parity bit of each stage
+    const int br = min(a.bs, kStep), nb = kStep / br;       // rows of a TMA box; boxes of a step
+
+    int n = sh.n;
+    long long off = sh.off, left = sh.end - sh.begin;
+    bool first_unit = true;
+    while (left > 0) {
+        const ReqWork rw = request_work(a, n);
+        if (off >= rw.work) {
+            off -= rw.work;
+            ++n;
+            continue;
+        }
+        // the unit (head, row tile) and its part of this share
+        const long long unit = off / rw.tiles;
+        const int tile0 = static_cast<int>(off - unit * rw.tiles);
+        const int ntile = static_cast<int>(min(left, static_cast<long long>(rw.tiles - tile0)));
+        const int h = static_cast<int>(unit / rw.row_tiles), rt = static_cast<int>(unit - static_cast<long long>(h) * rw.row_tiles);
+        const int rows = rw.qlen * G;
+        const int p_first = rw.kv - rw.qlen + rt * kRows / G;
+        const int p_last = rw.kv - rw.qlen + min(rt * kRows + kRows - 1, rows - 1) / G;
+        // tokens of this part that some row sees
+        const int t_lo = max((rw.tile0 + tile0) * kTile, a.window > 0 ? max(0, p_first - a.window + 1) / kTile * kTile : 0);
+        const int t_hi = min((rw.tile0 + tile0 + ntile) * kTile, p_last + 1);
+
+        W w;
+        const int *table = a.table + static_cast<long long>(n) * a.max_blocks;
+        // block numbers and scales of the warp's next 32 steps, one step a lane
+        struct Bank {
+            int blk[2];
+            float ksc[2], vsc[2];
+        } cur, nxt;
+        auto fetch_blocks = [&](Bank &bank, int step0) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int t = t_lo + (step0 + lane) * kTile + warp * kStep + b * br;
+                bank.blk[b] = -1;
+                bank.ksc[b] = bank.vsc[b] = 1.f;
+                if (b < nb && t < t_hi) {
+                    const int id = table[t >> a.bs_log2];
+                    if (id >= 0 && id < a.num_blocks) {
+                        bank.blk[b] = id;
+                        bank.ksc[b] = a.k_scale[static_cast<long long>(id) * a.Hkv + h];
+                        bank.vsc[b] = a.v_scale[static_cast<long long>(id) * a.Hkv + h];
+                    } else {
+                        atomicOr(a.err, kErrBadSeqlens);
+                    }
+                }
+            }
+        };
+        auto issue = [&](int i, const Bank &bank) {           // copies of step i
+            const int st = i % S::kStages, t = t_lo + i * kTile + warp * kStep;
+            const int b0 = __shfl_sync(0xffffffffu, bank.blk[0], i & 31);
+            const int b1 = __shfl_sync(0xffffffffu, bank.blk[1], i & 31);
+            const int boxes = (b0 >= 0) + (nb > 1 && b1 >= 0);
+            if (lane == 0 && boxes > 0) {
+                uint64_t *bar = &s_bar[warp][st];
+                const uint32_t dst = ring + st * S::kStageBytes;
+                mbar_arrive_expect_tx(bar, 2 * boxes * br * D);
+                const int r0 = t & (a.bs - 1);
+                if (b0 >= 0) {
+                    tma_load_2d(dst, &mk, bar, 0, ((b0 * a.Hkv + h) << a.bs_log2) + r0);
+                    tma_load_2d(dst + S::kStepBytes, &mv, bar, 0, ((b0 * a.Hkv + h) << a.bs_log2) + r0);
+                }
+                if (nb > 1 && b1 >= 0) {
+                    tma_load_2d(dst + br * D, &mk, bar, 0, (b1 * a.Hkv + h) << a.bs_log2);
+                    tma_load_2d(dst + S::kStepBytes + br * D, &mv, bar, 0, (b1 * a.Hkv + h) << a.bs_log2);
+                }
+            }
+            return boxes > 0;
+        };
+        // steps of this warp: those that start before t_hi
+        const int nstep = t_hi > t_lo + warp * kStep ? (t_hi - t_lo - warp * kStep + kTile - 1) / kTile : 0;
+        fetch_blocks(cur, 0);
+        nxt = cur;
+        uint32_t live = 0;                  // steps in flight that have copies, by stage
+        for (int i = 0; i < min(nstep, S::kStages - 1); ++i)
+            if (issue(i, cur)) live |= 1u << (i % S::kStages);
+
+        // queries, in fragment order: k-step 4 half + i, coordinates 16 (c + 4 half) + 4 i + 0 .. 3
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int R = rt * kRows + g + 8 * r;
+            const bool in = R < rows;
+            const int tok = R / G;
+            const IT *qp = static_cast<const IT *>(a.q) + (rw.row0 + tok) * a.q_stride +
+                           static_cast<long long>(h * G + (R - tok * G)) * D;
+            float f[D / 4];
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) load4(in ? qp + 16 * (c + 4 * half) + 4 * i : nullptr, &f[16 * half + 4 * i]);
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(f[i]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // a power of two 2^e with |q| < 2^(e + 1); infinities stay what they are
+            int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+            e = mx == 0.f || e > 127 ? 0 : max(e, -100);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - min(e, 126)) << 23);
+            w.rf[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + min(e, 126)) << 23);
+#pragma unroll
+            for (int s = 0; s < W::KS; ++s) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = f[4 * s + i] * inv;
+                if (QSPLIT) {
+                    split_h2(y[0], y[1], w.qa[s][r], w.ql[QSPLIT ? s : 0][r]);
+                    split_h2(y[2], y[3], w.qa[s][r + 2], w.ql[QSPLIT ? s : 0][r + 2]);
+                } else {
+                    w.qa[s][r] = pack_h2(y[0], y[1]);
+                    w.qa[s][r + 2] = pack_h2(y[2], y[3]);
+                }
+            }
+            w.hi[r] = in ? rw.kv - rw.qlen + tok : -1;
+            w.lo[r] = a.window > 0 ? w.hi[r] - a.window + 1 : 0;
+            w.m[r] = kNegInf;
+            w.l[r] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < W::NT; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
+        w.vu = 0.f;
+
+        const int lo_last = a.window > 0 ? p_last - a.window + 1 : 0;
+        bool ok = true;
+        for (int i = 0; i < nstep; ++i) {
+            const int st = i % S::kStages, t = t_lo + i * kTile + warp * kStep;
+            if ((i & 31) == 0 && i > 0) cur = nxt;
+            if ((i & 31) == 8 && i + 24 < nstep) fetch_blocks(nxt, i + 24);
+            const int b0 = __shfl_sync(0xffffffffu, cur.blk[0], i & 31);
+            const int b1 = __shfl_sync(0xffffffffu, cur.blk[1], i & 31);
+            float ks[2], vs[2];
+            ks[0] = __shfl_sync(0xffffffffu, cur.ksc[0], i & 31);
+            vs[0] = __shfl_sync(0xffffffffu, cur.vsc[0], i & 31);
+            ks[1] = ks[0];
+            vs[1] = vs[0];
+            uint32_t tok = b0 >= 0 ? 0xffffffffu : 0u;
+            if (nb > 1) {
+                ks[1] = __shfl_sync(0xffffffffu, cur.ksc[1], i & 31);
+                vs[1] = __shfl_sync(0xffffffffu, cur.vsc[1], i & 31);
+                tok = (b0 >= 0 ? 0xffffu : 0u) | (b1 >= 0 ? 0xffff0000u : 0u);
+            }
+            if (t_hi - t < kStep) tok &= (1u << (t_hi - t)) - 1u;
+            // the ring: the next step's copies go out before this one is waited for
+            __syncwarp();
+            const int nx = i + S::kStages - 1;
+            if (nx < nstep && ok) {
+                const uint32_t bit = 1u << (nx % S::kStages);
+                live = issue(nx, (nx >> 5) == (i >> 5) ? cur : nxt) ? live | bit : live & ~bit;
+            }
+            if (ok && (live & (1u << st))) {
+                const uint32_t par = (phase >> st) & 1u;
+                if (!ring_wait(&s_bar[warp][st], par, a.wait_limit)) {
+                    // gave up: reported, and the copy still in flight is waited for (with the drain's limit)
+                    // before its buffer is used again
+                    if (lane == 0) atomicOr(a.err, kErrWaitTimeout);
+                    ok = ring_wait(&s_bar[warp][st], par, kDrainLimitCycles);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                phase ^= 1u << st;
+            }
+            const uint32_t sk = ring + st * S::kStageBytes;
+            const bool edge = tok != 0xffffffffu || t + kStep - 1 > p_first || t < lo_last;
+            if (ok && tok != 0u) w.step(sk, sk + S::kStepBytes, t, ks, vs, tok, edge);
+        }
+
+        // ---- the four warps' parts of each row
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 2);
+            if (c == 0) {
+                s_ml[warp][g + 8 * r][0] = w.m[r];
+                s_ml[warp][g + 8 * r][1] = w.l[r];
+            }
+        }
+        __syncthreads();                    // every warp is through its ring
+        float *mg = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float *row = mg + (warp * kRows + g + 8 * r) * S::kMergeRow;
+            // n-tile i: column 2c is coordinate x0 + i, column 2c + 1 coordinate x1 + i
+            const int x0 = 16 * c, x1 = D == 128 ? 64 + 16 * c : 16 * c + 8;
+#pragma unroll
+            for (int i = 0; i < W::NT; i += 4) {
+                *reinterpret_cast<float4 *>(row + x0 + i) = make_float4(w.o[i][2 * r] * w.vu, w.o[i + 1][2 * r] * w.vu,
+                                                                        w.o[i + 2][2 * r] * w.vu, w.o[i + 3][2 * r] * w.vu);
+                *reinterpret_cast<float4 *>(row + x1 + i) =
+                    make_float4(w.o[i][2 * r + 1] * w.vu, w.o[i + 1][2 * r + 1] * w.vu, w.o[i + 2][2 * r + 1] * w.vu,
+                                w.o[i + 3][2 * r + 1] * w.vu);
+            }
+        }
+        __syncthreads();
+        const bool whole = tile0 == 0 && ntile == rw.tiles;
+        // a block leaves at most two parts: the end of a unit begun by another block (slot 0), and the start
+        // of one that another ends (slot 1; a middle piece goes to slot 0)
+        float *part = whole ? nullptr : a.ws + (2ll * blockIdx.x + (first_unit && tile0 > 0 ? 0 : 1)) * part_floats(D);
+        constexpr int TPR = kThreads / kRows;               // threads of a row
+        constexpr int CPT = D / TPR;                        // columns of a thread
+        const int r = tid / TPR, x = (tid % TPR) * CPT;
+        float mm = kNegInf;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) mm = fmaxf(mm, s_ml[q][r][0]);
+        const float base = mm == kNegInf ? 0.f : mm;
+        float ll = 0.f, acc[CPT];
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+            const float f = ex2(s_ml[q][r][0] - base);
+            ll = fmaf(s_ml[q][r][1], f, ll);
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) acc[i] = fmaf(mg[(q * kRows + r) * S::kMergeRow + x + i], f, acc[i]);
+        }
+        const int R = rt * kRows + r;
+        if (whole) {
+            if (R < rows) store_row<CPT>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
+        } else {
+            if (x == 0) { part[r] = mm; part[kRows + r] = ll; }
+#pragma unroll
+            for (int i = 0; i < CPT; i += 4)
+                *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + x + i) =
+                    make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        }
+        if (tile0 == 0 && ntile < rw.tiles)      // begun here, ended in a later share
+            cut = CutUnit{rw.row0, h, rt, min(kRows, rows - rt * kRows),
+                          static_cast<int>((sh.end - ntile + rw.tiles - 1) / sh.per) - static_cast<int>(blockIdx.x) + 1};
+        // the rings take copies again: what was read and written through the generic proxy comes before them
+        fence_proxy_async();
+        __syncthreads();
+        off += ntile;
+        left -= ntile;
+        first_unit = false;
+    }
+    if (tid == 0) a.cuts[blockIdx.x] = cut;
+}
+
+// Adds the parts of the units that were cut: block (c, y) takes four rows of the unit that starts in share c
+// and ends in a later one (the main kernel has noted which). A row's parts are taken in turn by kJoinWarps
+// warps, whose sums are added in warp order, so the order is fixed.
+constexpr int kJoinRows = 4, kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) kv_attn_join_kernel(const AttnArgs a) {
+    constexpr int CPL = D / 32;            // columns of a lane
+    __shared__ float s_ml[kJoinRows][kJoinWarps][2];
+    __shared__ float s_o[kJoinRows][kJoinWarps][D];
+    cudaGridDependencySynchronize();
+    const int blk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const CutUnit cu = a.cuts[blk];
+    const int rr = warp / kJoinWarps, pw = warp % kJoinWarps;
+    const int r = blockIdx.y * kJoinRows + rr;
+    if (cu.parts == 0 || blockIdx.y * kJoinRows >= cu.rows) return;
+
+    float m = kNegInf, l = 0.f, o[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int p = pw; p < cu.parts; p += kJoinWarps) {
+        const float *q = a.ws + (2ll * (blk + p) + (p == 0 ? 1 : 0)) * part_floats(D);
+        const float mp = q[r], lp = q[kRows + r];
+        float x[CPL];
+        const float *qo = q + 2 * kRows + r * D + lane * CPL;
+        if constexpr (D == 128) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(qo);
+        else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(qo);
+        const float mn = fmaxf(m, mp), base = mn == kNegInf ? 0.f : mn;
+        const float f = ex2(m - base), fp = ex2(mp - base);
+        m = mn;
+        l = l * f + lp * fp;
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) o[i] = o[i] * f + x[i] * fp;
+    }
+    if (lane == 0) { s_ml[rr][pw][0] = m; s_ml[rr][pw][1] = l; }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) s_o[rr][pw][lane * CPL + i] = o[i];
+    __syncthreads();
+    if (pw != 0 || lane >= D / 4 || r >= cu.rows) return;
+    float mm = kNegInf, ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kJoinWarps; ++q) mm = fmaxf(mm, s_ml[rr][q][0]);
+    const float base = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+    for (int q = 0; q < kJoinWarps; ++q) {
+        const float f = ex2(s_ml[rr][q][0] - base);
+        ll = fmaf(s_ml[rr][q][1], f, ll);
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s_o[rr][q][4 * lane + i], f, acc[i]);
+    }
+    const int G = a.Hq / a.Hkv, R = cu.row_tile * kRows + r;
+    store_row<4>(a, cu.row0 + R / G, cu.head * G + R % G, D, 4 * lane, acc, ll, mm);
+}
+
+template <int D, bool QSPLIT, bool PSPLIT, typename IT>
+gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
+    auto kern = kv_attn_kernel<D, QSPLIT, PSPLIT, IT>;
+    if (!ensure_smem_limit(reinterpret_cast<const void *>(kern), Smem<D>::kBytes)) return GDN_ERR_CUDA;
+    kern<<<grid, kThreads, Smem<D>::kBytes, stream>>>(mk, mv, a);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / kJoinRows);
+    cfg.blockDim = dim3(32 * kJoinRows * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D>, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <int D>
+gdn_status_t launch_d(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, bool in_f32,
+                      bool out_f32, cudaStream_t stream) {
+    if (in_f32) return out_f32 ? launch_t<D, true, true, float>(mk, mv, a, grid, stream)
+                               : launch_t<D, true, false, float>(mk, mv, a, grid, stream);
+    return out_f32 ? launch_t<D, false, true, __nv_bfloat16>(mk, mv, a, grid, stream)
+                   : launch_t<D, false, false, __nv_bfloat16>(mk, mv, a, grid, stream);
+}
+
+}  // namespace
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();      // tc_gdn.cu
+
+bool make_cache_map(CUtensorMap *m, const void *ptr, long long rows, int d, int box_rows) {
+    EncodeTiledFn encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int kv_attn_grid(int d) {
+    const int sms = sm_count();
+    return (sms > 0 ? sms : 148) * (d == 128 ? Smem<128>::kBlocks : Smem<64>::kBlocks);
+}
+
+size_t kv_attn_ws_bytes(int d) {
+    return static_cast<size_t>(kv_attn_grid(d)) * (2 * part_floats(d) * sizeof(float) + sizeof(CutUnit));
+}
+
+gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, bool in_f32, bool out_f32,
+                            cudaStream_t stream) {
+    a.err = device_error_word();
+    if (!a.err) return GDN_ERR_CUDA;
+    a.wait_limit = wait_limit_cycles();
+    const long long rows = static_cast<long long>(a.num_blocks) * a.Hkv * a.bs;
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, kc, rows, d, std::min(a.bs, kStep)) || !make_cache_map(&mv, vc, rows, d, std::min(a.bs, kStep)))
+        return GDN_ERR_CUDA;
+    const int grid = kv_attn_grid(d);
+    a.cuts = reinterpret_cast<CutUnit *>(a.ws + grid * 2 * part_floats(d));
+    return d == 128 ? launch_d<128>(mk, mv, a, grid, in_f32, out_f32, stream)
+                    : launch_d<64>(mk, mv, a, grid, in_f32, out_f32, stream);
+}
+
+}  // namespace gdn

@@ -363,13 +363,151 @@ gdn_status_t gdn_chunk_fwd_host(const void *q, const void *k, const void *v, con
                                 int B, int H, int L, int dk, int dv, int chunk, float scale, gdn_dtype_t in_dtype,
                                 int group, void *cuda_stream);
 
+/*
+ * Serving a batch of requests: hybrid models place softmax-attention layers between the
+ * linear-attention ones (page "【CS336】lecture4", the 7 : 1 and 3 : 1 mixes), and a serving
+ * step then needs, next to gdn_chunk_fwd_varlen and gdn_decode_step: the step's packed
+ * offsets and page tables (gdn_plan_batch), a paged cache for the softmax layers held in 8
+ * bits (gdn_kv_append) with the attention that reads it (gdn_kv_attn), and the delta-rule
+ * recurrence over a pool of states addressed by request (gdn_decode_slots).
+ *
+ * Token rows of these calls are token-major, (T, heads, d), as projections write them; a row
+ * stride in elements (>= heads * d) lets q, k and v be column ranges of one fused projection.
+ * Request n's rows are cu_seqlens[n] .. cu_seqlens[n+1]-1. Rows behind the last request are
+ * neither read nor written. Device-side checks: an offset, length, slot or block number
+ * outside its range is reported by the next gdn_sync_status() as GDN_ERR_INVALID_ARG and the
+ * request (or token, or block) it belongs to is left out; nothing is read or written for it.
+ *
+ * The cache: k_cache and v_cache (num_blocks, Hkv, block_size, d) e4m3 bytes, k_scale and
+ * v_scale (num_blocks, Hkv) fp32: one scale, a power of two, for each block of tokens and
+ * head. The cached value is code * scale. A request's position p is row p % block_size of the
+ * block block_table[n][p / block_size].
+ */
+
+/*
+ * gdn_plan_batch — block tables, slot maps and packed offsets of one step, on the device,
+ * from the requests' lengths. One call per step serves every layer.
+ *
+ *  ctx_lens    (N) int32: tokens of each request that the cache holds                read
+ *  new_lens    (N) int32: tokens it brings (0: it waits; -1: it has finished, and every
+ *              block of its table row goes back to the free list)                    read
+ *  block_table (N, max_blocks) int32, -1 where there is no block: blocks for the new
+ *              tokens are put in (entries that are there already are kept), a finished
+ *              request's row becomes -1                                           updated
+ *  free_list   (num_blocks) int32, a stack of free blocks, its top at free_count - 1:
+ *              finished requests push theirs first, in (request, block) order; new blocks
+ *              are popped in the same order                                        updated
+ *  free_count  (1) int32                                                           updated
+ *  T           rows of the step's token grid
+ *  cu_seqlens  (N + 1) int32: packed offsets of the new tokens (as the *_varlen calls
+ *              take them)                                                          written
+ *  kv_lens     (N) int32: ctx_lens + new tokens (0 for a finished request)         written
+ *  positions, seq_ids, slot_map  (T) int32: each row's position in its request, its
+ *              request, and its cache row block * block_size + position % block_size; -1 in
+ *              rows behind the last request                                        written
+ *  info        (4) int32: new tokens, the longest kv length, blocks that were missing,
+ *              free blocks left                                                    written
+ *  Too few free blocks: none is taken, info[2] says how many were missing, and tokens without
+ *  a block get slot -1 (the next call, with blocks freed, places them). More than T tokens in
+ *  all, or a length outside 0 .. max_blocks * block_size: GDN_ERR_INVALID_ARG from
+ *  gdn_sync_status; the step (or that request) brings no tokens.
+ *  A call may be captured; calls that share a table or free list must be ordered.
+ *  1 <= N <= 8192, block_size in {16, 32, 64, 128}, 0 <= T <= 2^30, max_blocks >= 1, num_blocks >= 1,
+ *  num_blocks * block_size and max_blocks * block_size < 2^31. Pointers 4-byte aligned.
+ */
+gdn_status_t gdn_plan_batch(const int *ctx_lens, const int *new_lens, int N, int *block_table, int max_blocks,
+                            int *free_list, int *free_count, int num_blocks, int block_size, int T, int *cu_seqlens,
+                            int *kv_lens, int *positions, int *seq_ids, int *slot_map, int *info, void *cuda_stream);
+
+/*
+ * gdn_kv_append — writes T new K and V rows into the cache at slot_map (as gdn_plan_batch
+ * makes it; -1: the row is skipped).
+ *
+ *  k, v       (T, Hkv, d) in_dtype, rows k_stride / v_stride elements apart            read
+ *  slot_map   (T) int32                                                                read
+ *  k_cache, v_cache, k_scale, v_scale   the cache                                   updated
+ *  A block's scale is the smallest power of two 2^e, e >= -100, with which its largest finite
+ *  |value| stays within 448; codes are rounded to nearest even. A run of rows that starts at
+ *  row 0 of a block starts it afresh; one that starts later keeps the block's scale unless a new
+ *  row needs a larger one, and the codes before it are then rescaled (exact, but for values
+ *  that fall below e4m3's smallest normal). NaN and infinities are stored as NaN and leave the
+ *  scale alone. Rows of a block behind the run keep their bytes.
+ *  The rows of one block must be consecutive rows of the call, with consecutive slots: a block
+ *  reached by two runs of one call has unspecified codes and scale.
+ *  T >= 0, Hkv >= 1, d in {64, 128}; k, v, caches 16-byte aligned, row strides a multiple of 16
+ *  bytes; scales and slot_map 4-byte aligned; num_blocks * block_size < 2^31.
+ */
+gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, long long v_stride, const int *slot_map,
+                           void *k_cache, void *v_cache, float *k_scale, float *v_scale, int T, int Hkv, int d,
+                           int num_blocks, int block_size, gdn_dtype_t in_dtype, void *cuda_stream);
+
+/*
+ * gdn_kv_attn — causal softmax attention of each request's newest tokens over its cached keys
+ * and values, the new tokens' own among them (append first):
+ *     o_i = sum_p w_ip v_p / sum_p w_ip,  w_ip = exp(scale q_i . k_p),  lse_i = log sum_p w_ip
+ * over the positions p <= pos_i (and p > pos_i - window when window > 0), pos_i = kv_lens[n] -
+ * (rows of request n) + i for row i of request n. Query head h reads KV head h / (Hq / Hkv).
+ * A query that sees nothing (pos_i < 0) gets o = 0, lse = -inf.
+ *
+ *  q            (T, Hq, d) in_dtype, rows q_stride elements apart                     read
+ *  block_table  (N, max_blocks) int32; entries of positions < kv_lens[n] are read     read
+ *  cu_seqlens   (N + 1) int32, kv_lens (N) int32                                      read
+ *  o            (T, Hq, d) out_dtype                                               written
+ *  lse          (T, Hq) fp32, nullable                                             written
+ *  max_q_len    an upper bound of the rows of one request, >= 1: it chooses between the forms
+ *               for few and for many rows; a request with more rows than it says is left out
+ *               and reported as malformed
+ *  workspace    device memory of at least gdn_kv_attn_workspace_bytes(...) bytes, 16-byte
+ *               aligned, owned by the caller; contents irrelevant on entry and unspecified on
+ *               return. Calls that may overlap on the GPU need one each.
+ *  Sums and softmax statistics are fp32. bf16 queries enter the products exactly; fp32 ones as
+ *  two fp16 parts (22 bits). The weights enter them as fp16 with a bf16 output, and as two
+ *  fp16 parts with an fp32 one. A position that a query does not see does not reach its
+ *  result, whatever its values.
+ *  N >= 1, T >= 0, 1 <= Hkv <= Hq, Hq % Hkv == 0, Hq <= 65535, d in {64, 128}, block_size in
+ *  {16, 32, 64, 128}, window >= 0, scale finite; num_blocks * Hkv * block_size and max_blocks *
+ *  block_size < 2^31; q, o, caches 16-byte aligned, the row stride of q a multiple of 16 bytes.
+ */
+size_t gdn_kv_attn_workspace_bytes(int N, int T, int Hq, int Hkv, int d, int max_q_len);
+gdn_status_t gdn_kv_attn(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
+                         const float *k_scale, const float *v_scale, const int *block_table, const int *cu_seqlens,
+                         const int *kv_lens, void *o, float *lse, void *workspace, size_t workspace_bytes, int N, int T,
+                         int Hq, int Hkv, int d, int num_blocks, int block_size, int max_blocks, int max_q_len,
+                         int window, float scale, gdn_dtype_t in_dtype, gdn_dtype_t out_dtype, void *cuda_stream);
+
+/*
+ * gdn_decode_slots — the recurrence of gdn_decode_step over a pool of states addressed by
+ * slot, any number of tokens for each request, key heads shared by value heads: value head h
+ * reads key head h / (Hv / Hk). Each request's state is read once and written once.
+ *
+ *  q, k       (T, Hk, dk), v (T, Hv, dv) in_dtype; rows q_stride, k_stride, v_stride elements
+ *             apart                                                                    read
+ *  beta, g    (T, Hv) fp32, nullable as in gdn_decode_step (g (T, Hv, dk) with
+ *             opts->g_per_key)                                                         read
+ *  state      (n_slots, Hv, dk, dv) fp32                                            updated
+ *  slots      (N) int32: request n's state; -1: request n is skipped (its rows of o are left
+ *             as they were). A slot named twice belongs to the first request that names it;
+ *             the others are left out and reported as malformed.
+ *  cu_seqlens (N + 1) int32, nullable: request n's rows (NULL: row n alone, T = N). A request
+ *             without rows leaves its state as it was.
+ *  o          (T, Hv, dv) fp32 or opts->out_dtype                                   written
+ *  opts       nullable, as in gdn_decode_step_ex (d_skip and xnorm_weight are (Hv, dv))
+ *  N, Hk >= 1, T >= 0, Hv % Hk == 0, Hv <= 65535, n_slots >= 1, dk, dv in {64, 128}; q, k, v,
+ *  state, o 16-byte aligned, beta, g, slots, cu_seqlens 4-byte aligned.
+ */
+gdn_status_t gdn_decode_slots(const void *q, const void *k, const void *v, long long q_stride, long long k_stride,
+                              long long v_stride, const float *beta, const float *g, float *state, const int *slots,
+                              const int *cu_seqlens, void *o, int N, int T, int Hk, int Hv, int n_slots, int dk, int dv,
+                              float scale, gdn_dtype_t in_dtype, const gdn_fwd_opts_t *opts, void *cuda_stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *gdn_status_str(gdn_status_t status);
 
 /*
  * gdn_sync_status — synchronise `cuda_stream`, then report and clear one device-side
  * condition met by a kernel of this library on the current device since it was last
- * reported, in this order: GDN_ERR_INVALID_ARG for a malformed cu_seqlens list,
+ * reported, in this order: GDN_ERR_INVALID_ARG for a malformed cu_seqlens list (or a length,
+ * slot or block number out of range in the serving calls),
  * GDN_ERR_TIMEOUT for a bounded wait that gave up, GDN_ERR_BOUNDS (only in the library built
  * with -DGDN_DEBUG_BOUNDS, libgdn_debug.so) when a kernel's global access index fell outside
  * the extent its launch implies, GDN_ERR_NONFINITE when a tensor-core
