@@ -35,6 +35,7 @@ constexpr int kStep = 32;                   // tokens of a warp's step
 constexpr int kTile = kStep * kWarps;       // tokens of a block's tile
 constexpr int kRows = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kSlack = 8.f;               // a row's exponents may pass its reference by this much
 
 template <int D> struct Smem {
     static constexpr int kBlocks = D == 128 ? 2 : 3;         // blocks an SM holds (registers)
@@ -89,6 +90,26 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, long l
     } while (!mbar_try_wait(b, parity));
     return true;
 }
+// the same for an e4m3 query: D += A (16 x 32, e4m3) B (32 x 8, e4m3)
+__device__ __forceinline__ void mma16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the two e4m3 codes in the low half -> fp16 pair (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(w));
+    return h;
+}
+// four values -> four e4m3 codes, nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t e4m3x4(const float (&y)[4]) {
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y[1]), "f"(y[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y[3]), "f"(y[2]));
+    return a | (static_cast<uint32_t>(b) << 16);
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -106,29 +127,92 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t h) {      // 0xffff in t
     return __hneu2_mask(x, x);
 }
 
-// A block's row state while a unit runs, and the loop over its steps.
-template <int D, bool QSPLIT, bool PSPLIT>
+// How queries enter Q K^T. kF8: as two e4m3 parts (bf16 queries with a bf16 output: the codes of K are then an
+// operand as they are); kF16, kF16x2: as one or two fp16 parts, K's codes converted.
+enum QKind { kF8, kF16, kF16x2 };
+
+// A warp's row state while a unit runs, and its steps.
+template <int D, QKind QK, bool PSPLIT>
 struct Worker {
-    static constexpr int KS = D / 16;          // k-steps of Q K^T
-    static constexpr int NT = D / 8;           // n-tiles of P V
-    uint32_t qa[KS][4], ql[QSPLIT ? KS : 1][4];
+    static constexpr int KS = QK == kF8 ? D / 32 : D / 16;     // k-steps of Q K^T
+    static constexpr int NT = D / 8;                           // n-tiles of P V
+    uint32_t qa[KS][4], ql[QK == kF16 ? 1 : KS][4];            // queries, high and low parts
     float o[NT][4];
-    float m[2], l[2], rf[2];                   // rows g and g + 8: maximum, this lane's part of the sum, score factor
-    int hi[2], lo[2];                          // positions a row sees: lo .. hi
-    float vu;                                  // V scale that the accumulators are in units of (0: none yet)
+    float m[2], l[2], rf[2];       // rows g and g + 8: reference of the exponents, this lane's part of the sum, score factor
+    int hi[2], lo[2];              // positions a row sees: lo .. hi
+    float vu;                      // V scale that the accumulators are in units of (0: none yet)
 
     __device__ __forceinline__ static int token_of(int n) { return D == 128 ? (n & 1) * 4 + (n >> 1) : n; }
 
-    // one step: 32 tokens from position t0; sk, sv: shared addresses of the codes; ks, vs: the scales of the
-    // step's two halves; tok: tokens that exist (bit i: t0 + i); edge: some row does not see some token
+    __device__ __forceinline__ void scale_o(float f0, float f1) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            o[i][0] *= f0; o[i][1] *= f0; o[i][2] *= f1; o[i][3] *= f1;
+        }
+    }
+
+    // Queries of row g + 8 r from this lane's D / 4 coordinates (lane c: coordinates 16 (c + 4 half) + 0 .. 15).
+    __device__ __forceinline__ void set_query(int r, const float (&f)[D / 4], float scale_log2) {
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(f[i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // a power of two 2^e: |q| 2^-e < 2 for fp16 parts, <= 448 for e4m3 ones
+        const uint32_t u = __float_as_uint(mx);
+        int e = static_cast<int>(u >> 23) - 127;
+        if (QK == kF8) e += ((u & 0x7fffffu) > 0x600000u ? 1 : 0) - 8;
+        e = mx == 0.f || u >= 0x7f800000u ? 0 : min(max(e, -100), 126);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        rf[r] = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if constexpr (QK == kF8) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {         // coordinates 8 s + 4 half + 0 .. 3
+                    float y[4], z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = f[8 * s + 4 * half + i] * inv;
+                        if (fabsf(y[i]) > 448.f) y[i] = __int_as_float(0x7fffffff);      // an infinite query shows as NaN
+                    }
+                    const uint32_t h = e4m3x4(y);
+                    uint32_t lo2, hi2;
+                    e4m3_to_h2(h, lo2, hi2);
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&lo2));
+                    const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&hi2));
+                    z[0] = y[0] - p.x; z[1] = y[1] - p.y; z[2] = y[2] - q.x; z[3] = y[3] - q.y;
+                    qa[s][r + 2 * half] = h;
+                    ql[s][r + 2 * half] = e4m3x4(z);
+                }
+        } else {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = f[4 * s + i] * inv;
+                if constexpr (QK == kF16x2) {
+                    split_h2(y[0], y[1], qa[s][r], ql[s][r]);
+                    split_h2(y[2], y[3], qa[s][r + 2], ql[s][r + 2]);
+                } else {
+                    qa[s][r] = pack_h2(y[0], y[1]);
+                    qa[s][r + 2] = pack_h2(y[2], y[3]);
+                }
+            }
+        }
+    }
+
+    // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's two
+    // halves; EDGE: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
+    template <bool EDGE>
     __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[2], const float (&vs)[2],
-                                         uint32_t tok, bool edge) {
+                                         uint32_t tok) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-        float s[4][4];
+        float x[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 8 * j + token_of(g);
-            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half) {
                 const int swz = D == 128 ? (r & 7) : ((r >> 1) & 3);
@@ -136,72 +220,88 @@ struct Worker {
                 asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                              : "r"(sk + r * D + (((c + 4 * half) ^ swz) << 4)));
+                if constexpr (QK == kF8) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mma16832(x[j], qa[2 * half + i], w[2 * i], w[2 * i + 1]);
+                        mma16832(x[j], ql[2 * half + i], w[2 * i], w[2 * i + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b0, b1;
+                        e4m3_to_h2(w[i], b0, b1);
+                        mma16816(x[j], qa[4 * half + i], b0, b1);
+                        if constexpr (QK == kF16x2) mma16816(x[j], ql[4 * half + i], b0, b1);
+                    }
+                }
+            }
+        }
+        // Base-2 exponents against the row's reference m; elements 0, 1: row g, tokens token_of(2c), token_of(2c + 1),
+        // 2, 3: row g + 8. The reference moves only when an exponent passes kSlack (fp16 holds weights up to 2^15), so
+        // that most steps neither reduce over the row's lanes nor touch the accumulators.
+        auto sees = [&](int j, int i) {
+            const int t = 8 * j + token_of(2 * c + (i & 1));
+            return ((tok >> t) & 1u) && t0 + t <= hi[i >> 1] && t0 + t >= lo[i >> 1];
+        };
+        const bool none[2] = {m[0] == kNegInf, m[1] == kNegInf};      // rows without a reference yet
+        float top = kNegInf;
+        {
+            const float base[2] = {none[0] ? 0.f : m[0], none[1] ? 0.f : m[1]};
+            const float rk[2][2] = {{rf[0] * ks[0], rf[1] * ks[0]}, {rf[0] * ks[1], rf[1] * ks[1]}};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t b0, b1;
-                    e4m3_to_h2(w[i], b0, b1);
-                    mma16816(s[j], qa[4 * half + i], b0, b1);
-                    if (QSPLIT) mma16816(s[j], ql[4 * half + i], b0, b1);
+                    x[j][i] = fmaf(x[j][i], rk[j >> 1][i >> 1], -base[i >> 1]);
+                    if (EDGE) x[j][i] = sees(j, i) ? x[j][i] : kNegInf;
+                    top = fmaxf(top, x[j][i]);
                 }
-            }
         }
-        // scores in base-2 exponents; c0, c1: row g, tokens token_of(2c), token_of(2c + 1); c2, c3: row g + 8
-        float mx[2] = {kNegInf, kNegInf};
+        if (__any_sync(0xffffffffu, top > kSlack || none[0] || none[1])) {
+            float f[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int r = 0; r < 2; ++r) {
+                float mx = kNegInf;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x = s[j][i] * (rf[i >> 1] * ks[j >> 1]);
-                if (edge) {
-                    const int t = 8 * j + token_of(2 * c + (i & 1));
-                    const bool see = ((tok >> t) & 1u) && t0 + t <= hi[i >> 1] && t0 + t >= lo[i >> 1];
-                    x = see ? x : kNegInf;
+                for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[j][2 * r], x[j][2 * r + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                f[r] = 1.f;
+                if (mx > (none[r] ? kNegInf : 0.f)) {
+                    f[r] = none[r] ? 0.f : ex2(-mx);
+                    m[r] = none[r] ? mx : m[r] + mx;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) { x[j][2 * r] -= mx; x[j][2 * r + 1] -= mx; }
                 }
-                s[j][i] = x;
-                mx[i >> 1] = fmaxf(mx[i >> 1], x);
+                l[r] *= f[r];
             }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        }
-        float fac[2], base[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float mn = fmaxf(m[r], mx[r]);
-            base[r] = mn == kNegInf ? 0.f : mn;
-            fac[r] = ex2(m[r] - base[r]);
-            m[r] = mn;
-            l[r] *= fac[r];
+            scale_o(f[0], f[1]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[j][i] = ex2(s[j][i] - base[i >> 1]);
-                l[i >> 1] += s[j][i];
+                x[j][i] = ex2(x[j][i]);
+                l[i >> 1] += x[j][i];
             }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
-            const float u = vu == 0.f ? 1.f : vu / vs[hf];
-            vu = vs[hf];
-            const float f0 = (hf == 0 ? fac[0] : 1.f) * u, f1 = (hf == 0 ? fac[1] : 1.f) * u;
-            if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    o[i][0] *= f0; o[i][1] *= f0; o[i][2] *= f1; o[i][3] *= f1;
-                }
+            if (vs[hf] != vu) {
+                const float u = vu == 0.f ? 1.f : vu / vs[hf];
+                scale_o(u, u);
+                vu = vs[hf];
             }
             uint32_t p[4], pl[4];
-            float(&x)[4] = s[2 * hf], (&y)[4] = s[2 * hf + 1];
-            if (PSPLIT) {
-                split_h2(x[0], x[1], p[0], pl[0]);
-                split_h2(x[2], x[3], p[1], pl[1]);
-                split_h2(y[0], y[1], p[2], pl[2]);
-                split_h2(y[2], y[3], p[3], pl[3]);
+            float(&xa)[4] = x[2 * hf], (&xb)[4] = x[2 * hf + 1];
+            if constexpr (PSPLIT) {
+                split_h2(xa[0], xa[1], p[0], pl[0]);
+                split_h2(xa[2], xa[3], p[1], pl[1]);
+                split_h2(xb[0], xb[1], p[2], pl[2]);
+                split_h2(xb[2], xb[3], p[3], pl[3]);
             } else {
-                p[0] = pack_h2(x[0], x[1]); p[1] = pack_h2(x[2], x[3]);
-                p[2] = pack_h2(y[0], y[1]); p[3] = pack_h2(y[2], y[3]);
+                p[0] = pack_h2(xa[0], xa[1]); p[1] = pack_h2(xa[2], xa[3]);
+                p[2] = pack_h2(xb[0], xb[1]); p[3] = pack_h2(xb[2], xb[3]);
             }
             // this lane's four V rows of the half: k = 2c, 2c + 1, 2c + 8, 2c + 9
             const int ra = 16 * hf + token_of(2 * c), rb = 16 * hf + token_of(2 * c + 1);
@@ -221,11 +321,14 @@ struct Worker {
                                  : "r"(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
                 }
             }
-            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu}, seen[4] = {};
             bool nans = false;
-            if (edge) {        // rows that do not exist hold anything: their values are taken out
-                keep0 = (((tok >> ra) & 1u) ? 0xffffu : 0u) | (((tok >> rb) & 1u) ? 0xffff0000u : 0u);
-                keep1 = (((tok >> (ra + 8)) & 1u) ? 0xffffu : 0u) | (((tok >> (rb + 8)) & 1u) ? 0xffff0000u : 0u);
+            if constexpr (EDGE) {
+                // Rows that do not exist hold anything: their values are taken out. A NaN among values that some row
+                // does not see must reach the rows that do, and 0 * NaN must not reach the others: where there is one,
+                // its rows are those with a 1 (token seen) against a 1 (a NaN there).
+                keep[0] = (((tok >> ra) & 1u) ? 0xffffu : 0u) | (((tok >> rb) & 1u) ? 0xffff0000u : 0u);
+                keep[1] = (((tok >> (ra + 8)) & 1u) ? 0xffffu : 0u) | (((tok >> (rb + 8)) & 1u) ? 0xffff0000u : 0u);
                 bool any = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -235,58 +338,55 @@ struct Worker {
                         any |= ((z - 0x01010101u) & ~z & 0x80808080u) != 0u;
                     }
                 nans = __any_sync(0xffffffffu, any);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (sees(2 * hf + (r >> 1), 2 * (r & 1) + e)) seen[r] |= 0x3c00u << (16 * e);
             }
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                uint32_t e[4][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e4m3_to_h2(v[i][w], e[i][0], e[i][1]);
+            for (int w = 0; w < W; ++w)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t b0 = __byte_perm(e[0][q >> 1], e[1][q >> 1], q & 1 ? 0x7632 : 0x5410);
-                    uint32_t b1 = __byte_perm(e[2][q >> 1], e[3][q >> 1], q & 1 ? 0x7632 : 0x5410);
+                    // column 4 w + q of the lane's chunk: the two rows' bytes side by side, then as fp16 pair
+                    const uint32_t sel = q | ((4 + q) << 4);
+                    uint32_t b0 = e4m3x2_to_h2(__byte_perm(v[0][w], v[1][w], sel));
+                    uint32_t b1 = e4m3x2_to_h2(__byte_perm(v[2][w], v[3][w], sel));
                     float(&acc)[4] = o[4 * w + q];
-                    if (edge) {
-                        b0 &= keep0;
-                        b1 &= keep1;
+                    if constexpr (EDGE) {
+                        b0 &= keep[0];
+                        b1 &= keep[1];
                         if (nans) {
-                            // a NaN among values that some row does not see: it must reach the rows that do, and
-                            // 0 * NaN must not reach the others. The rows it reaches are those with a 1 (a token
-                            // seen) against a 1 (a NaN there).
                             const uint32_t n0 = nan_halves(b0), n1 = nan_halves(b1);
                             b0 &= ~n0;
                             b1 &= ~n1;
-                            uint32_t seen[4];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                uint32_t bits = 0u;
-#pragma unroll
-                                for (int e2 = 0; e2 < 2; ++e2) {
-                                    const int t = 16 * hf + 8 * (r >> 1) + token_of(2 * c + e2);
-                                    const bool see = ((tok >> t) & 1u) && t0 + t <= hi[r & 1] && t0 + t >= lo[r & 1];
-                                    if (see) bits |= 0x3c00u << (16 * e2);
-                                }
-                                seen[r] = bits;
-                            }
                             float hit[4] = {0.f, 0.f, 0.f, 0.f};
                             mma16816(hit, seen, n0 & 0x3c003c00u, n1 & 0x3c003c00u);
 #pragma unroll
                             for (int r = 0; r < 4; ++r) acc[r] = hit[r] > 0.f ? __int_as_float(0x7fffffff) : acc[r];
                         }
                     }
-                    mma16816(acc, p, b0, b1);
-                    if (PSPLIT) mma16816(acc, pl, b0, b1);
+                    if constexpr (PSPLIT) {
+                        // an fp32 output: the tensor core's own running sum truncates, so each half's sum starts anew
+                        // and is added in fp32
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma16816(t, pl, b0, b1);
+                        mma16816(t, p, b0, b1);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[r] += t[r];
+                    } else {
+                        mma16816(acc, p, b0, b1);
+                    }
                 }
-            }
         }
     }
 };
 
-template <int D, bool QSPLIT, bool PSPLIT, typename IT>
+template <int D, QKind QK, bool PSPLIT, typename IT>
 __global__ void __launch_bounds__(kThreads, Smem<D>::kBlocks)
 kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
     using S = Smem<D>;
-    using W = Worker<D, QSPLIT, PSPLIT>;
+    using W = Worker<D, QK, PSPLIT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t s_bar[kWarps][S::kStages];
     __shared__ Share s_share;
@@ -322,9 +422,14 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             continue;
         }
         // the unit (head, row tile) and its part of this share
-        const long long unit = off / rw.tiles;
-        const int tile0 = static_cast<int>(off - unit * rw.tiles);
-        const int ntile = static_cast<int>(min(left, static_cast<long long>(rw.tiles - tile0)));
+        const int cost = rw.tiles + kUnitCost;
+        const long long unit = off / cost;
+        const int at = static_cast<int>(off - unit * cost);
+        const int take = static_cast<int>(min(left, static_cast<long long>(cost - at)));
+        const int tile0 = max(0, at - kUnitCost), ntile = max(0, at + take - kUnitCost) - tile0;
+        off += take;
+        left -= take;
+        if (ntile == 0) continue;           // the share ends before the unit's first tile
         const int h = static_cast<int>(unit / rw.row_tiles), rt = static_cast<int>(unit - static_cast<long long>(h) * rw.row_tiles);
         const int rows = rw.qlen * G;
         const int p_first = rw.kv - rw.qlen + rt * kRows / G;
@@ -400,29 +505,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             for (int half = 0; half < D / 64; ++half)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) load4(in ? qp + 16 * (c + 4 * half) + 4 * i : nullptr, &f[16 * half + 4 * i]);
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(f[i]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // a power of two 2^e with |q| < 2^(e + 1); infinities stay what they are
-            int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            e = mx == 0.f || e > 127 ? 0 : max(e, -100);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - min(e, 126)) << 23);
-            w.rf[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + min(e, 126)) << 23);
-#pragma unroll
-            for (int s = 0; s < W::KS; ++s) {
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = f[4 * s + i] * inv;
-                if (QSPLIT) {
-                    split_h2(y[0], y[1], w.qa[s][r], w.ql[QSPLIT ? s : 0][r]);
-                    split_h2(y[2], y[3], w.qa[s][r + 2], w.ql[QSPLIT ? s : 0][r + 2]);
-                } else {
-                    w.qa[s][r] = pack_h2(y[0], y[1]);
-                    w.qa[s][r + 2] = pack_h2(y[2], y[3]);
-                }
-            }
+            w.set_query(r, f, a.scale_log2);
             w.hi[r] = in ? rw.kv - rw.qlen + tok : -1;
             w.lo[r] = a.window > 0 ? w.hi[r] - a.window + 1 : 0;
             w.m[r] = kNegInf;
@@ -472,7 +555,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             const uint32_t sk = ring + st * S::kStageBytes;
             const bool edge = tok != 0xffffffffu || t + kStep - 1 > p_first || t < lo_last;
-            if (ok && tok != 0u) w.step(sk, sk + S::kStepBytes, t, ks, vs, tok, edge);
+            if (ok && tok != 0u) {
+                if (edge) w.template step<true>(sk, sk + S::kStepBytes, t, ks, vs, tok);
+                else w.template step<false>(sk, sk + S::kStepBytes, t, ks, vs, tok);
+            }
         }
 
         // ---- the four warps' parts of each row
@@ -535,12 +621,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         }
         if (tile0 == 0 && ntile < rw.tiles)      // begun here, ended in a later share
             cut = CutUnit{rw.row0, h, rt, min(kRows, rows - rt * kRows),
-                          static_cast<int>((sh.end - ntile + rw.tiles - 1) / sh.per) - static_cast<int>(blockIdx.x) + 1};
+                          static_cast<int>((sh.end + rw.tiles - ntile - 1) / sh.per) - static_cast<int>(blockIdx.x) + 1};
         // the rings take copies again: what was read and written through the generic proxy comes before them
         fence_proxy_async();
         __syncthreads();
-        off += ntile;
-        left -= ntile;
         first_unit = false;
     }
     if (tid == 0) a.cuts[blockIdx.x] = cut;
@@ -599,9 +683,9 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) kv_attn_join_kern
     store_row<4>(a, cu.row0 + R / G, cu.head * G + R % G, D, 4 * lane, acc, ll, mm);
 }
 
-template <int D, bool QSPLIT, bool PSPLIT, typename IT>
+template <int D, QKind QK, bool PSPLIT, typename IT>
 gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
-    auto kern = kv_attn_kernel<D, QSPLIT, PSPLIT, IT>;
+    auto kern = kv_attn_kernel<D, QK, PSPLIT, IT>;
     if (!ensure_smem_limit(reinterpret_cast<const void *>(kern), Smem<D>::kBytes)) return GDN_ERR_CUDA;
     kern<<<grid, kThreads, Smem<D>::kBytes, stream>>>(mk, mv, a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
@@ -620,10 +704,10 @@ gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnAr
 template <int D>
 gdn_status_t launch_d(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, bool in_f32,
                       bool out_f32, cudaStream_t stream) {
-    if (in_f32) return out_f32 ? launch_t<D, true, true, float>(mk, mv, a, grid, stream)
-                               : launch_t<D, true, false, float>(mk, mv, a, grid, stream);
-    return out_f32 ? launch_t<D, false, true, __nv_bfloat16>(mk, mv, a, grid, stream)
-                   : launch_t<D, false, false, __nv_bfloat16>(mk, mv, a, grid, stream);
+    if (in_f32) return out_f32 ? launch_t<D, kF16x2, true, float>(mk, mv, a, grid, stream)
+                               : launch_t<D, kF16x2, false, float>(mk, mv, a, grid, stream);
+    return out_f32 ? launch_t<D, kF16, true, __nv_bfloat16>(mk, mv, a, grid, stream)
+                   : launch_t<D, kF8, false, __nv_bfloat16>(mk, mv, a, grid, stream);
 }
 
 }  // namespace

@@ -31,8 +31,12 @@ bool make_cache_map(CUtensorMap *m, const void *ptr, long long rows, int d, int 
 // Floats of one partial: m and l of 16 rows, then their O.
 __host__ __device__ constexpr long long part_floats(int d) { return 32 + 16ll * d; }
 
-// A request's part of the work line: (Hkv x row_tiles) units of `tiles` kv tiles (128 tokens each) from
-// tile0 on. A request with rows has one tile at least, so that every unit's rows are written.
+// What a unit costs beside its tiles (its queries, the warps' merge, its rows), in tiles. Without it the shares of
+// short contexts took longest.
+constexpr int kUnitCost = 2;
+
+// A request's part of the work line: (Hkv x row_tiles) units of kUnitCost + `tiles` places, a place for each kv tile
+// (128 tokens) from tile0 on. A request with rows has one tile at least, so that every unit's rows are written.
 struct ReqWork {
     long long row0;     // first token row
     int qlen, kv, row_tiles, tiles, tile0;
@@ -52,7 +56,7 @@ __device__ __forceinline__ ReqWork request_work(const AttnArgs &a, int n) {
     w.tile0 = 0;
     if (a.window > 0) w.tile0 = static_cast<int>(max(0ll, static_cast<long long>(w.kv) - w.qlen - a.window + 1) / 128);
     w.tiles = max(1, (w.kv + 127) / 128 - w.tile0);
-    w.work = static_cast<long long>(a.Hkv) * w.row_tiles * w.tiles;
+    w.work = static_cast<long long>(a.Hkv) * w.row_tiles * (w.tiles + kUnitCost);
     w.bad = bad;
     return w;
 }
