@@ -733,9 +733,15 @@ static int kv_attn_grid(int d) {
     return (sms > 0 ? sms : 148) * (d == 128 ? Smem<128>::kBlocks : Smem<64>::kBlocks);
 }
 
-size_t kv_attn_ws_bytes(int d) {
-    return static_cast<size_t>(kv_attn_grid(d)) * (2 * part_floats(d) * sizeof(float) + sizeof(CutUnit));
+size_t kv_attn_ws_bytes(int N, int d) {
+    return static_cast<size_t>(kv_attn_grid(d)) * (2 * part_floats(d) * sizeof(float) + sizeof(CutUnit)) +
+           (static_cast<size_t>(N) * sizeof(int) + 15) / 16 * 16;
 }
+
+// kv_prompt.cu: requests of more than a.many_rows rows (bf16 in and out); redo: (N) ints, zeroed by it
+gdn_status_t launch_kv_prompt(const void *kc, const void *vc, const AttnArgs &a, int d, int *redo, cudaStream_t stream);
+
+constexpr int kManyRows = 64;
 
 gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, bool in_f32, bool out_f32,
                             cudaStream_t stream) {
@@ -748,6 +754,14 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
         return GDN_ERR_CUDA;
     const int grid = kv_attn_grid(d);
     a.cuts = reinterpret_cast<CutUnit *>(a.ws + grid * 2 * part_floats(d));
+    int *redo = reinterpret_cast<int *>(a.cuts + grid);
+    a.redo = redo;
+    a.many_rows = 0;
+    if (!in_f32 && !out_f32 && static_cast<long long>(a.max_q) * (a.Hq / a.Hkv) > kManyRows) {
+        a.many_rows = kManyRows;
+        const gdn_status_t st = launch_kv_prompt(kc, vc, a, d, redo, stream);
+        if (st != GDN_OK) return st;
+    }
     return d == 128 ? launch_d<128>(mk, mv, a, grid, in_f32, out_f32, stream)
                     : launch_d<64>(mk, mv, a, grid, in_f32, out_f32, stream);
 }

@@ -21,6 +21,9 @@ struct AttnArgs {
     CutUnit *cuts;
     int N, T, Hq, Hkv, num_blocks, bs, bs_log2, max_blocks, max_q, window, out_bf16;
     float scale_log2;          // scale * log2(e): scores are kept as base-2 exponents
+    // requests of more rows than this belong to the many-rows kernel (0: it is not used), but for those it left
+    int many_rows;
+    const int *redo;           // (N), nullable: requests that the many-rows kernel left
     unsigned *err;
     long long wait_limit;
 };
@@ -41,9 +44,9 @@ struct ReqWork {
     long long row0;     // first token row
     int qlen, kv, row_tiles, tiles, tile0;
     long long work;
-    bool bad;
+    bool bad, many;
 };
-__device__ __forceinline__ ReqWork request_work(const AttnArgs &a, int n) {
+__device__ __forceinline__ ReqWork request_work(const AttnArgs &a, int n, bool many_kernel = false) {
     ReqWork w;
     const int c0 = a.cu[n], c1 = a.cu[n + 1];
     w.row0 = c0;
@@ -52,6 +55,8 @@ __device__ __forceinline__ ReqWork request_work(const AttnArgs &a, int n) {
     const bool bad = c0 < 0 || c1 < c0 || c1 > a.T || w.qlen > a.max_q || w.kv < 0 ||
                      w.kv > static_cast<long long>(a.max_blocks) * a.bs;
     if (bad) w.qlen = 0;
+    w.many = !bad && a.many_rows > 0 && static_cast<long long>(w.qlen) * (a.Hq / a.Hkv) > a.many_rows;
+    if (w.many && !many_kernel && !a.redo[n]) w.qlen = 0;
     w.row_tiles = static_cast<int>((static_cast<long long>(w.qlen) * (a.Hq / a.Hkv) + 15) / 16);
     w.tile0 = 0;
     if (a.window > 0) w.tile0 = static_cast<int>(max(0ll, static_cast<long long>(w.kv) - w.qlen - a.window + 1) / 128);

@@ -1,0 +1,621 @@
+// gdn_kv_attn, many rows a request (a prompt's chunk), bf16 queries and output: the same attention on the
+// tensor cores' tcgen05 path.
+//
+// A block takes 256 rows (row R: token R / G, query head R % G of one KV head) as two groups of 128, each a
+// 128-row UMMA tile, and walks the 128-token tiles of the cache that some row sees:
+//   S = Q K^T   kind::f8f6f4: the cache's codes are the operand as TMA brings them; queries are the sum of
+//               two e4m3 parts (row scaled by a power of two), so two products into one accumulator
+//   P = 2^(S rk - m)   rk: row and block scale; m: a reference that moves only when an exponent passes it
+//               by kSlack, so that the accumulators are rarely rescaled; P as fp16 over S in tensor memory
+//   O += P V    kind::f16: V's codes converted to fp16 in shared memory once for both groups, times the
+//               block's scale over the unit's largest (a power of two: exact)
+// Scores cannot be in fp32 here (two e4m3 parts hold a bf16 query exactly down to 2^-9 of its row's largest
+// element, and within 2^-18 of it below), which is why other types take the few-rows kernel.
+//
+// What bounds it: per tile and group the two products take 1024 cycles of the tensor pipe and the 16384
+// exponentials 1024 of the special-function units, so the two groups' softmax and products are interleaved:
+// one group's exponentials run under the other's products.
+//
+// Warps: 0 TMA and block scales, 1 UMMA issue, 2 tensor memory, 4-7 V conversion, 8-11 and 12-15 the groups.
+// Tensor memory: S (and P over it) of each group, O of each group, 512 columns at d = 128.
+//
+// Two inputs do not fit this scheme, and their request is left to the few-rows kernel, which runs after
+// this one and computes it again: V scales of one unit more than 2^12 apart (fp16 would lose the small ones),
+// and NaN codes in V (0 * NaN would reach rows that do not see them).
+#include <algorithm>
+
+#include "kv_attn.cuh"
+#include "tc_ctl.cuh"
+
+namespace gdn {
+namespace {
+using namespace ptx;
+
+constexpr int kThreads = 512;
+constexpr int kTok = 128;                 // tokens of a tile
+constexpr int kGroupRows = 128, kUnitRows = 256;
+constexpr int kKStages = 3, kVStages = 2, kKsSlots = 8;
+constexpr float kSlack = 8.f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMinScale = 7.888609052210118e-31f;      // 2^-100: a block of zeros
+constexpr float kSpread = 4096.f;
+
+enum : int {
+    B_Q = 0,          // 8 warps: queries written
+    B_KF = 1,         // [3] K tile (and its scales) in
+    B_KE = 4,         // [3] both groups' products with it done
+    B_VF = 7,         // [2] V codes in
+    B_VE = 9,         // [2] converted
+    B_CF = 11,        // [2] fp16 V written
+    B_CE = 13,        // [2] both groups' products with it done
+    B_S = 15,         // [2 groups] scores done
+    B_P = 17,         // [2 groups] weights written, accumulators rescaled
+    B_O = 19,         // [2 groups] P V done
+    B_END = 21,       // everything issued is done
+    B_KS = 22,        // [8] K scales of a tile written
+    kNumBars = 30
+};
+
+template <int D> struct Lay {
+    static constexpr uint32_t kTile8 = kTok * D, kTile16 = kTok * D * 2;
+    static constexpr uint32_t OFF_Q = 0;                                  // [group][hi, lo] 128 x D
+    static constexpr uint32_t OFF_K = 4 * kGroupRows * D;
+    static constexpr uint32_t OFF_V8 = OFF_K + kKStages * kTile8;
+    static constexpr uint32_t OFF_V = OFF_V8 + kVStages * kTile8;         // halves of 64 columns, 128 rows x 128 B
+    static constexpr uint32_t OFF_KS = OFF_V + kVStages * kTile16;        // K scales of 16-token groups, and which exist
+    static constexpr uint32_t OFF_BAR = OFF_KS + kKsSlots * 9 * 4;
+    static constexpr uint32_t kBytes = OFF_BAR + kNumBars * 8 + 64;
+    static constexpr uint32_t kAlloc = kBytes + 1024;
+    static_assert(OFF_K % 1024 == 0 && OFF_V8 % 1024 == 0 && OFF_V % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
+    static_assert(kAlloc <= 232448, "shared memory");
+    static constexpr uint32_t TM_S = 0, TM_O = 256;                       // + 128 (S), + D (O) for the second group
+};
+
+// D[tmem] (+)= A[smem] B[smem]^T, e4m3 operands, fp32 accumulation
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);   // e4m3: 0
+}
+// K-major tile of D-byte rows: 128-byte swizzle at D = 128, 64-byte at D = 64
+template <int D> __device__ __forceinline__ uint64_t kdesc(uint32_t addr) {
+    uint64_t d = sdesc_sw128(addr, 16, 8 * D);
+    if (D == 64) d = (d & ~(7ull << 61)) | (4ull << 61);
+    return d;
+}
+// byte offset of 16-byte chunk c of row r in such a tile
+template <int D> __device__ __forceinline__ uint32_t kswz(uint32_t r, uint32_t c) {
+    return D == 128 ? sw128(r, c) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+    uint32_t u[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x4(const float (&y)[4]) {
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y[1]), "f"(y[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y[3]), "f"(y[2]));
+    return a | (static_cast<uint32_t>(b) << 16);
+}
+__device__ __forceinline__ void e4m3_to_h2(uint32_t w, __half2 &lo, __half2 &hi) {
+    uint32_t a, b;
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "mov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+    lo = *reinterpret_cast<const __half2 *>(&a);
+    hi = *reinterpret_cast<const __half2 *>(&b);
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+
+// The request and row tile (of 256 rows) with index `idx` among those of this kernel, last tiles (the longest) first.
+struct Unit {
+    int n, rt;
+};
+__device__ __forceinline__ bool find_unit(const AttnArgs &a, int idx, Unit *out) {
+    __shared__ int s_sum[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
+    const int per = (a.N + kThreads - 1) / kThreads;
+    const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
+    auto tiles = [&](int n) {
+        const ReqWork w = request_work(a, n, true);
+        return w.many ? static_cast<int>((static_cast<long long>(w.qlen) * G + kUnitRows - 1) / kUnitRows) : 0;
+    };
+    int own = 0;
+    for (int n = n0; n < n1; ++n) own += tiles(n);
+    int inc = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    if (tid == 0) out->n = -1;
+    __syncthreads();
+    int before = inc - own, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const int at = total - 1 - idx;
+    if (at >= before && at < before + own) {
+        int n = n0, b = before;
+        for (int c = tiles(n); at >= b + c; c = tiles(n)) { b += c; ++n; }
+        out->n = n;
+        out->rt = at - b;
+    }
+    __syncthreads();
+    return at >= 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a,
+                 int *__restrict__ redo) {
+    using L = Lay<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    float *s_ks = reinterpret_cast<float *>(smem + L::OFF_KS);                       // [slot][8]
+    uint32_t *s_have = reinterpret_cast<uint32_t *>(s_ks + kKsSlots * 8);            // [slot]
+    __shared__ Unit s_unit;
+    __shared__ unsigned s_vmax, s_vmin;
+    const Ctl ctl{bars, abort_flag, a.err, a.wait_limit};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.Hq / a.Hkv, h = blockIdx.x % a.Hkv;
+
+    if (tid == 0) {
+        for (int b = 0; b < kNumBars; ++b)
+            mbar_init(&bars[b], b == B_Q ? 8 : (b >= B_VE && b < B_CE) || (b >= B_P && b < B_O) ? 4 : 1);
+        *abort_flag = 0;
+        s_vmax = __float_as_uint(kMinScale);
+        s_vmin = 0x7f800000u;
+        fence_mbar_init();
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mv);
+    }
+    if (!find_unit(a, blockIdx.x / a.Hkv, &s_unit)) return;
+    const Unit u = s_unit;
+    const ReqWork rw = request_work(a, u.n, true);
+    const int rows = rw.qlen * G, p0 = rw.kv - rw.qlen;
+    // positions of each group's first and last row, and its tiles
+    int pf[2], pl[2], ta[2], tb[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int r0 = u.rt * kUnitRows + g * kGroupRows, r1 = min(r0 + kGroupRows, rows) - 1;
+        pf[g] = p0 + r0 / G;
+        pl[g] = r1 >= r0 ? p0 + r1 / G : -1;
+        tb[g] = pl[g] >= 0 ? pl[g] / kTok + 1 : 0;
+        ta[g] = a.window > 0 ? min(tb[g], max(0, pf[g] - a.window + 1) / kTok) : 0;
+    }
+    if (tb[1] == 0) ta[1] = tb[1] = tb[0];               // no rows: after the other's tiles
+    if (tb[0] == 0) ta[0] = tb[0] = ta[1];
+    const int t_a = ta[0], nt = tb[1] - ta[0];           // tiles t_a .. t_a + nt - 1
+    const int t_hi = max(pl[0], pl[1]) + 1;
+    const int *table = a.table + static_cast<long long>(u.n) * a.max_blocks;
+
+    // V's largest scale here, and the smallest of a block that is not all zeros
+    {
+        float mx = kMinScale, mn = __int_as_float(0x7f800000);
+        const int b1 = (t_hi + a.bs - 1) >> a.bs_log2;
+        for (int b = ((t_a * kTok) >> a.bs_log2) + tid; b < b1; b += kThreads) {
+            const int id = table[b];
+            if (id < 0 || id >= a.num_blocks) { atomicOr(a.err, kErrBadSeqlens); continue; }
+            const float s = a.v_scale[static_cast<long long>(id) * a.Hkv + h];
+            mx = fmaxf(mx, s);
+            if (s > kMinScale) mn = fminf(mn, s);
+        }
+        atomicMax(&s_vmax, __float_as_uint(mx));
+        atomicMin(&s_vmin, __float_as_uint(mn));
+    }
+    __syncthreads();
+    const float vu = __uint_as_float(s_vmax);
+    if (vu > kSpread * __uint_as_float(s_vmin)) {         // fp16 would lose the smaller blocks
+        if (tid == 0) redo[u.n] = 1;
+        return;
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ================================================================ TMA, K scales
+        const int bl = a.bs >> 4;                        // 16-token groups of a block
+        int id_next = -1;
+        auto look = [&](int j) {                         // block of this lane's 16-token group of tile j
+            const int t = (t_a + j) * kTok + 16 * lane;
+            int id = -1;
+            if (lane < 8 && j < nt && t < t_hi) {
+                id = table[t >> a.bs_log2];
+                if (id >= a.num_blocks) id = -1;
+            }
+            return id;
+        };
+        id_next = look(0);
+        int last = -1;
+        bool ok = true;
+        for (int j = 0; j < nt && ok; ++j) {
+            const int id = id_next, t = (t_a + j) * kTok + 16 * lane;
+            const float ks = id >= 0 ? a.k_scale[static_cast<long long>(id) * a.Hkv + h] : 1.f;
+            id_next = look(j + 1);
+            const bool box = id >= 0 && lane % bl == 0;
+            const uint32_t boxes = __ballot_sync(0xffffffffu, box), have = __ballot_sync(0xffffffffu, id >= 0);
+            const uint32_t bytes = __popc(boxes) * a.bs * D;
+            const int row = ((id * a.Hkv + h) << a.bs_log2) + (t & (a.bs - 1));
+            const int ksl = j % kKStages, vsl = j % kVStages;
+            if (j >= kKStages) ok = ctl.wait(B_KE + ksl, (j / kKStages - 1) & 1);
+            if (j >= kVStages && ok) ok = ctl.wait(B_VE + vsl, (j / kVStages - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane < 8) s_ks[(j % kKsSlots) * 8 + lane] = ks;
+            if (lane == 0) s_have[j % kKsSlots] = have;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[B_KS + j % kKsSlots]);
+                mbar_arrive_expect_tx(&bars[B_KF + ksl], bytes);
+                mbar_arrive_expect_tx(&bars[B_VF + vsl], bytes);
+            }
+            __syncwarp();
+            if (box) {
+                tma_2d(sb + L::OFF_K + ksl * L::kTile8 + 16 * lane * D, &mk, &bars[B_KF + ksl], 0, row);
+                tma_2d(sb + L::OFF_V8 + vsl * L::kTile8 + 16 * lane * D, &mv, &bars[B_VF + vsl], 0, row);
+            }
+            last = j;
+        }
+        // never leave a copy in flight past the end of the block
+        for (int j = max(0, last - kKStages + 1); j <= last; ++j) ctl.drain(B_KF + j % kKStages, (j / kKStages) & 1);
+        for (int j = max(0, last - kVStages + 1); j <= last; ++j) ctl.drain(B_VF + j % kVStages, (j / kVStages) & 1);
+    } else if (warp == 1) {
+        // ================================================================ UMMA issue
+        if (lane == 0 && nt > 0) {
+            constexpr uint32_t kIdS = idesc_e4m3(128, kTok), kIdO = idesc_f16(128, D, false, true);
+            int np[2] = {0, 0};                          // P V products issued, by group
+            auto scores = [&](int g, int j) {            // S_g = Q_g K_j^T
+                const uint32_t kt = sb + L::OFF_K + (j % kKStages) * L::kTile8, qt = sb + L::OFF_Q + g * 2 * kGroupRows * D;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_f8(tmem + L::TM_S + g * 128, kdesc<D>(qt + part * kGroupRows * D + kk * 32), kdesc<D>(kt + kk * 32),
+                               kIdS, part + kk > 0);
+                mma_commit(&bars[B_S + g]);
+            };
+            bool ok = ctl.wait(B_Q, 0) && ctl.wait(B_KF, 0);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    if (t_a >= ta[g] && t_a < tb[g]) scores(g, 0);
+                mma_commit(&bars[B_KE]);
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                const int tile = t_a + j, vsl = j % kVStages;
+                ok = ctl.wait(B_CF + vsl, (j / kVStages) & 1);
+                if (ok && j + 1 < nt) ok = ctl.wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (tile >= ta[g] && tile < tb[g]) {
+                        ok = ctl.wait(B_P + g, np[g] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t vt = sb + L::OFF_V + vsl * L::kTile16;
+#pragma unroll
+                        for (int kk = 0; kk < kTok / 16; ++kk)
+                            mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + kk * 8,
+                                       sdesc_sw128(vt + kk * 2048, 16384, 1024), kIdO, np[g] > 0 || kk > 0);
+                        mma_commit(&bars[B_O + g]);
+                        ++np[g];
+                    }
+                    if (j + 1 < nt && tile + 1 >= ta[g] && tile + 1 < tb[g]) {
+                        // the scores go where P lies, which the product just issued still reads
+                        if (np[g] > 0) ok = ctl.wait(B_O + g, (np[g] - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(g, j + 1);
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&bars[B_CE + vsl]);
+                if (j + 1 < nt) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
+            }
+            mma_commit(&bars[B_END]);
+            ctl.drain(B_END, 0);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ================================================================ V: codes -> fp16, a token a thread
+        const int tk = tid - 128;
+        auto look = [&](int j, float &s) {               // whether the token exists, and its factor
+            const int t = (t_a + j) * kTok + tk;
+            s = 0.f;
+            if (j >= nt || t >= t_hi) return false;
+            const int id = table[t >> a.bs_log2];
+            if (id < 0 || id >= a.num_blocks) return false;
+            s = a.v_scale[static_cast<long long>(id) * a.Hkv + h] / vu;
+            return true;
+        };
+        float s_next;
+        bool e_next = look(0, s_next), ok = true, nan = false;
+        for (int j = 0; j < nt && ok; ++j) {
+            const int sl = j % kVStages;
+            const float s = s_next;
+            const bool e = e_next;
+            ok = ctl.wait(B_VF + sl, (j / kVStages) & 1);
+            if (ok && j >= kVStages) ok = ctl.wait(B_CE + sl, (j / kVStages - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            e_next = look(j + 1, s_next);
+            const __half2 f = __float2half2_rn(s);
+            __half2 probe = __float2half2_rn(0.f);
+            const uint8_t *src = smem + L::OFF_V8 + sl * L::kTile8;
+            uint8_t *dst = smem + L::OFF_V + sl * L::kTile16;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                uint4 w = *reinterpret_cast<const uint4 *>(src + kswz<D>(tk, c));
+                if (!e) w = make_uint4(0u, 0u, 0u, 0u);  // rows that do not exist hold anything
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    __half2 lo, hi;
+                    e4m3_to_h2(x[i], lo, hi);
+                    lo = __hmul2(lo, f);
+                    hi = __hmul2(hi, f);
+                    probe = __hfma2(lo, __float2half2_rn(0.f), probe);
+                    probe = __hfma2(hi, __float2half2_rn(0.f), probe);
+                    y[2 * i] = h2u(lo);
+                    y[2 * i + 1] = h2u(hi);
+                }
+                // 16 columns: two chunks of the 64-column half c / 4
+                uint8_t *half = dst + (c >> 2) * 16384;
+                *reinterpret_cast<uint4 *>(half + sw128(tk, (2 * c) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(half + sw128(tk, (2 * c + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            nan |= __half2float(__low2half(probe)) != 0.f || __half2float(__high2half(probe)) != 0.f;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[B_CF + sl]);
+                mbar_arrive(&bars[B_VE + sl]);
+            }
+        }
+        if (nan) redo[u.n] = 1;
+    } else if (warp >= 8) {
+        // ================================================================ a group's rows, one a thread
+        const int g = (warp - 8) >> 2, r = tid - 256 - g * 128;
+        const int R = u.rt * kUnitRows + g * kGroupRows + r;
+        const bool in = R < rows;
+        const int tok = R / G;
+        const long long token = rw.row0 + tok;
+        const int head = h * G + (R - tok * G);
+        const uint32_t trow = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + trow + L::TM_S + g * 128, to = tmem + trow + L::TM_O + g * D;
+        float rf;
+        {
+            const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + token * a.q_stride +
+                                                              static_cast<long long>(head) * D);
+            uint4 w[D / 8];
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                w[i] = in ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xffff0000u))));
+            }
+            const uint32_t ub = __float_as_uint(mx);
+            int e = static_cast<int>(ub >> 23) - 127 - 8 + ((ub & 0x7fffffu) > 0x600000u ? 1 : 0);
+            e = mx == 0.f || ub >= 0x7f800000u ? 0 : min(max(e, -100), 126);
+            // the score factor is kept positive (a negative scale goes into the query), so that a column group's
+            // largest product is also its largest score
+            const float inv = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), a.scale_log2);
+            rf = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            uint8_t *qh = smem + L::OFF_Q + g * 2 * kGroupRows * D, *ql = qh + kGroupRows * D;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x0 = k < 2 ? (k == 0 ? w[2 * c].x : w[2 * c].z) : (k == 2 ? w[2 * c + 1].x : w[2 * c + 1].z);
+                    const uint32_t x1 = k < 2 ? (k == 0 ? w[2 * c].y : w[2 * c].w) : (k == 2 ? w[2 * c + 1].y : w[2 * c + 1].w);
+                    float y[4] = {__uint_as_float(x0 << 16) * inv, __uint_as_float(x0 & 0xffff0000u) * inv,
+                                  __uint_as_float(x1 << 16) * inv, __uint_as_float(x1 & 0xffff0000u) * inv};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (fabsf(y[i]) > 448.f) y[i] = __int_as_float(0x7fffffff);      // an infinite query shows as NaN
+                    hi[k] = e4m3x4(y);
+                    __half2 p, q;
+                    e4m3_to_h2(hi[k], p, q);
+                    const float2 pf2 = __half22float2(p), qf2 = __half22float2(q);
+                    const float z[4] = {y[0] - pf2.x, y[1] - pf2.y, y[2] - qf2.x, y[3] - qf2.y};
+                    lo[k] = e4m3x4(z);
+                }
+                *reinterpret_cast<uint4 *>(qh + kswz<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(ql + kswz<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_Q]);
+        }
+        const int hi = in ? p0 + tok : -1, lo = a.window > 0 ? hi - a.window + 1 : 0;
+        const int lo_last = a.window > 0 ? pl[g] - a.window + 1 : 0;
+        float m = kNegInf, l = 0.f;
+        int done = 0;                                    // tiles of this group so far
+        bool ok = true;
+        for (int tile = ta[g]; tile < tb[g] && ok; ++tile, ++done) {
+            const int j = tile - t_a, t0 = tile * kTok, slot = j % kKsSlots;
+            ok = ctl.wait(B_KS + slot, (j / kKsSlots) & 1) && ctl.wait(B_S + g, done & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t have = s_have[slot];
+            const bool edge = have != 0xffu || t0 + kTok - 1 > pf[g] || t0 < lo_last;
+            const int c_hi = hi - t0, c_lo = lo - t0;    // columns this row sees
+            auto mask = [&](float (&s)[32], int ch) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int c = 32 * ch + i;
+                    s[i] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[i] : kNegInf;
+                }
+            };
+            // the largest exponent
+            float top = kNegInf;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(ts + 32 * ch, s);
+                tmem_wait_ld();
+                if (edge) mask(s, ch);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * hf + i], s[16 * hf + 8 + i]);
+#pragma unroll
+                    for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+                        for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
+                    if (x[0] > kNegInf) top = fmaxf(top, x[0] * (rf * s_ks[slot * 8 + 2 * ch + hf]));
+                }
+            }
+            const bool none = m == kNegInf;
+            const bool move = none ? top > kNegInf : top > m + kSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                float f = 1.f;
+                if (move) {
+                    f = none ? 0.f : ex2(m - top);
+                    m = top;
+                    l *= f;
+                }
+                if (done > 0) {                          // rescale the row's accumulators: P V before this must be done
+                    ok = ctl.wait(B_O + g, (done - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        float o[16];
+                        tmem_ld16(to + 16 * ch, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                        tmem_st16(to + 16 * ch, o);
+                    }
+                }
+            }
+            const float base = m == kNegInf ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(ts + 32 * ch, s);
+                tmem_wait_ld();
+                if (edge) mask(s, ch);
+                const float k0 = rf * s_ks[slot * 8 + 2 * ch], k1 = rf * s_ks[slot * 8 + 2 * ch + 1];
+                float p[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float x = ex2(fmaf(s[i], i < 16 ? k0 : k1, -base)), y = ex2(fmaf(s[i + 1], i < 16 ? k0 : k1, -base));
+                    sum[(i >> 1) & 3] += x + y;
+                    p[i >> 1] = __uint_as_float(pack_h2(x, y));
+                }
+                tmem_st16(ts + 16 * ch, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_P + g]);
+        }
+        if (ok && done > 0) ok = ctl.wait(B_O + g, (done - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : vu / l;
+        __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + (token * a.Hq + head) * D;
+        if (ok) {
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float o[32];
+                if (done > 0) {
+                    tmem_ld32(to + 32 * ch, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(l == 0.f ? 0.f : o[i + 2 * k] * inv,
+                                                                       l == 0.f ? 0.f : o[i + 2 * k + 1] * inv);
+                        w[k] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    if (in) *reinterpret_cast<uint4 *>(op + 32 * ch + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (in && a.lse) a.lse[token * a.Hq + head] = l == 0.f ? kNegInf : 0.6931471805599453f * (m + log2f(l));
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int *redo, cudaStream_t stream) {
+    auto kern = kv_prompt_kernel<D>;
+    if (!ensure_smem_limit(reinterpret_cast<const void *>(kern), Lay<D>::kAlloc)) return GDN_ERR_CUDA;
+    // no more units than this, whatever the lengths are: a request that comes here has more than many_rows rows
+    const long long all = static_cast<long long>(a.T) * (a.Hq / a.Hkv);
+    const long long units = (all / kUnitRows + std::min<long long>(a.N, all / a.many_rows)) * a.Hkv;
+    if (units > 2147483647ll) return GDN_ERR_UNSUPPORTED;
+    if (cudaMemsetAsync(redo, 0, static_cast<size_t>(a.N) * sizeof(int), stream) != cudaSuccess) return GDN_ERR_CUDA;
+    kern<<<static_cast<unsigned>(units), kThreads, Lay<D>::kAlloc, stream>>>(mk, mv, a, redo);
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+gdn_status_t launch_kv_prompt(const void *kc, const void *vc, const AttnArgs &a, int d, int *redo, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(a.num_blocks) * a.Hkv * a.bs;
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, kc, rows, d, a.bs) || !make_cache_map(&mv, vc, rows, d, a.bs)) return GDN_ERR_CUDA;
+    return d == 128 ? launch_t<128>(mk, mv, a, redo, stream) : launch_t<64>(mk, mv, a, redo, stream);
+}
+
+}  // namespace gdn

@@ -10,7 +10,7 @@ gdn_status_t launch_plan(const int *ctx, const int *add, int N, int *table, int 
 gdn_status_t launch_kv_append(const void *k, const void *v, long long ks, long long vs, const int *slot, void *kc,
                               void *vc, float *ksc, float *vsc, int T, int H, int d, int num_blocks, int block_size,
                               gdn_dtype_t in_dtype, cudaStream_t stream);
-size_t kv_attn_ws_bytes(int d);
+size_t kv_attn_ws_bytes(int N, int d);
 gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, bool in_f32, bool out_f32,
                             cudaStream_t stream);
 gdn_status_t launch_decode_slots(const void *q, const void *k, const void *v, long long qs, long long ks, long long vs,
@@ -72,7 +72,7 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
 
 size_t gdn_kv_attn_workspace_bytes(int N, int T, int Hq, int Hkv, int d, int max_q_len) {
     if (N < 1 || T < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !head_ok(d) || max_q_len < 1) return 0;
-    return gdn::kv_attn_ws_bytes(d);
+    return gdn::kv_attn_ws_bytes(N, d);
 }
 
 gdn_status_t gdn_kv_attn(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
