@@ -252,7 +252,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-
+    // The groups keep a row's 128 scores in registers: 256 threads take 192 each, the other 256 64 (65536 in all, what
+    // the block was launched with)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
         // ================================================================ TMA, K scales
         const int bl = a.bs >> 4;                        // 16-token groups of a block
@@ -359,6 +361,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
     } else if (warp >= 4 && warp < 8) {
         // ================================================================ V: codes -> fp16, a token a thread
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         const int tk = tid - 128;
         auto look = [&](int j, float &s) {               // whether the token exists, and its factor
             const int t = (t_a + j) * kTok + tk;
@@ -417,6 +420,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         if (nan) redo[u.n] = 1;
     } else if (warp >= 8) {
         // ================================================================ a group's rows, one a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int g = (warp - 8) >> 2, r = tid - 256 - g * 128;
         const int R = u.rt * kUnitRows + g * kGroupRows + r;
         const bool in = R < rows;
@@ -487,32 +491,27 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const uint32_t have = s_have[slot];
             const bool edge = have != 0xffu || t0 + kTok - 1 > pf[g] || t0 < lo_last;
             const int c_hi = hi - t0, c_lo = lo - t0;    // columns this row sees
-            auto mask = [&](float (&s)[32], int ch) {
+            // the row's 128 scores, and the largest exponent
+            float s[kTok];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int c = 32 * ch + i;
-                    s[i] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[i] : kNegInf;
-                }
-            };
-            // the largest exponent
-            float top = kNegInf;
+            for (int ch = 0; ch < 4; ++ch) tmem_ld32(ts + 32 * ch, *reinterpret_cast<float (*)[32]>(s + 32 * ch));
+            tmem_wait_ld();
+            if (edge) {
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                tmem_ld32(ts + 32 * ch, s);
-                tmem_wait_ld();
-                if (edge) mask(s, ch);
+                for (int c = 0; c < kTok; ++c) s[c] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[c] : kNegInf;
+            }
+            float top = kNegInf, k[8];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float x[8];
+            for (int q = 0; q < 8; ++q) {
+                k[q] = rf * s_ks[slot * 8 + q];
+                float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * hf + i], s[16 * hf + 8 + i]);
+                for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * q + i], s[16 * q + 8 + i]);
 #pragma unroll
-                    for (int w = 4; w >= 1; w >>= 1)
+                for (int w = 4; w >= 1; w >>= 1)
 #pragma unroll
-                        for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
-                    if (x[0] > kNegInf) top = fmaxf(top, x[0] * (rf * s_ks[slot * 8 + 2 * ch + hf]));
-                }
+                    for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
+                if (x[0] > kNegInf) top = fmaxf(top, x[0] * k[q]);
             }
             const bool none = m == kNegInf;
             const bool move = none ? top > kNegInf : top > m + kSlack;
@@ -543,15 +542,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                tmem_ld32(ts + 32 * ch, s);
-                tmem_wait_ld();
-                if (edge) mask(s, ch);
-                const float k0 = rf * s_ks[slot * 8 + 2 * ch], k1 = rf * s_ks[slot * 8 + 2 * ch + 1];
                 float p[16];
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float x = ex2(fmaf(s[i], i < 16 ? k0 : k1, -base)), y = ex2(fmaf(s[i + 1], i < 16 ? k0 : k1, -base));
+                    const int c = 32 * ch + i;
+                    const float x = ex2(fmaf(s[c], k[c >> 4], -base)), y = ex2(fmaf(s[c + 1], k[c >> 4], -base));
                     sum[(i >> 1) & 3] += x + y;
                     p[i >> 1] = __uint_as_float(pack_h2(x, y));
                 }
