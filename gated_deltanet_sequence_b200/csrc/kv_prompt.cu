@@ -363,26 +363,30 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // ================================================================ V: codes -> fp16, a token a thread
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         const int tk = tid - 128;
-        auto look = [&](int j, float &s) {               // whether the token exists, and its factor
+        // Its block's number is loaded two tiles ahead and the block's scale one tile ahead, both used no sooner: a load
+        // that an instruction of the same tile waited for would hold up the conversion (1300 cycles a tile).
+        auto block_of = [&](int j) {
             const int t = (t_a + j) * kTok + tk;
-            s = 0.f;
-            if (j >= nt || t >= t_hi) return false;
-            const int id = table[t >> a.bs_log2];
-            if (id < 0 || id >= a.num_blocks) return false;
-            s = a.v_scale[static_cast<long long>(id) * a.Hkv + h] / vu;
-            return true;
+            return j < nt && t < t_hi ? table[t >> a.bs_log2] : -1;
         };
-        float s_next;
-        bool e_next = look(0, s_next), ok = true, nan = false;
+        auto scale_of = [&](int id) {
+            return id >= 0 && id < a.num_blocks ? a.v_scale[static_cast<long long>(id) * a.Hkv + h] : -1.f;
+        };
+        const float inv_vu = 1.f / vu;
+        float s_next = scale_of(block_of(0));             // negative: the token does not exist
+        int id_next = block_of(1);
+        bool ok = true, nan = false;
         for (int j = 0; j < nt && ok; ++j) {
             const int sl = j % kVStages;
-            const float s = s_next;
-            const bool e = e_next;
+            const float s_raw = s_next;
+            s_next = scale_of(id_next);
+            id_next = block_of(j + 2);
             ok = ctl.wait(B_VF + sl, (j / kVStages) & 1);
             if (ok && j >= kVStages) ok = ctl.wait(B_CE + sl, (j / kVStages - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            e_next = look(j + 1, s_next);
+            const bool e = s_raw >= 0.f;
+            const float s = fmaxf(s_raw, 0.f) * inv_vu;   // exact: powers of two
             const __half2 f = __float2half2_rn(s);
             __half2 probe = __float2half2_rn(0.f);
             const uint8_t *src = smem + L::OFF_V8 + sl * L::kTile8;
