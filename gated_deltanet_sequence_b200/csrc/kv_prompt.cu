@@ -34,7 +34,7 @@ using namespace ptx;
 constexpr int kThreads = 512;
 constexpr int kTok = 128;                 // tokens of a tile
 constexpr int kGroupRows = 128, kUnitRows = 256;
-constexpr int kKStages = 3, kVStages = 2, kKsSlots = 8;
+constexpr int kKStages = 2, kVStages = 2, kCStages = 3, kKsSlots = 8;   // K and V codes, fp16 V, K scales
 constexpr float kSlack = 8.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMinScale = 7.888609052210118e-31f;      // 2^-100: a block of zeros
@@ -42,12 +42,12 @@ constexpr float kSpread = 4096.f;
 
 enum : int {
     B_Q = 0,          // 8 warps: queries written
-    B_KF = 1,         // [3] K tile (and its scales) in
-    B_KE = 4,         // [3] both groups' products with it done
-    B_VF = 7,         // [2] V codes in
-    B_VE = 9,         // [2] converted
-    B_CF = 11,        // [2] fp16 V written
-    B_CE = 13,        // [2] both groups' products with it done
+    B_KF = 1,         // [2] K tile in
+    B_KE = 3,         // [2] both groups' products with it done
+    B_VF = 5,         // [2] V codes in
+    B_VE = 7,         // [2] converted
+    B_CF = 9,         // [3] fp16 V written
+    B_CE = 12,        // [3] both groups' products with it done
     B_S = 15,         // [2 groups] scores done
     B_P = 17,         // [2 groups] weights written, accumulators rescaled
     B_O = 19,         // [2 groups] P V done
@@ -62,7 +62,7 @@ template <int D> struct Lay {
     static constexpr uint32_t OFF_K = 4 * kGroupRows * D;
     static constexpr uint32_t OFF_V8 = OFF_K + kKStages * kTile8;
     static constexpr uint32_t OFF_V = OFF_V8 + kVStages * kTile8;         // halves of 64 columns, 128 rows x 128 B
-    static constexpr uint32_t OFF_KS = OFF_V + kVStages * kTile16;        // K scales of 16-token groups, and which exist
+    static constexpr uint32_t OFF_KS = OFF_V + kCStages * kTile16;        // K scales of 16-token groups, and which exist
     static constexpr uint32_t OFF_BAR = OFF_KS + kKsSlots * 9 * 4;
     static constexpr uint32_t kBytes = OFF_BAR + kNumBars * 8 + 64;
     static constexpr uint32_t kAlloc = kBytes + 1024;
@@ -78,6 +78,11 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);   // e4m3: 0
@@ -304,60 +309,78 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int j = max(0, last - kVStages + 1); j <= last; ++j) ctl.drain(B_VF + j % kVStages, (j / kVStages) & 1);
     } else if (warp == 1) {
         // ================================================================ UMMA issue
-        if (lane == 0 && nt > 0) {
+        // The whole warp runs the loop and one elected lane issues: in code the compiler knows to be uniform the
+        // descriptors live in uniform registers (issued by a lane of a divergent branch, an instruction took 130
+        // cycles for the pipe's 65).
+        if (nt > 0) {
             constexpr uint32_t kIdS = idesc_e4m3(128, kTok), kIdO = idesc_f16(128, D, false, true);
+            const bool leader = elect_one();
+            const uint64_t dq = kdesc<D>(sb + L::OFF_Q), dk = kdesc<D>(sb + L::OFF_K), dv = sdesc_sw128(sb + L::OFF_V, 16384, 1024);
             int np[2] = {0, 0};                          // P V products issued, by group
+            auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, ctl.wait(b, parity)) != 0; };
             auto scores = [&](int g, int j) {            // S_g = Q_g K_j^T
-                const uint32_t kt = sb + L::OFF_K + (j % kKStages) * L::kTile8, qt = sb + L::OFF_Q + g * 2 * kGroupRows * D;
+                const uint64_t qd = dq + ((g * 2 * kGroupRows * D) >> 4), kd = dk + ((j % kKStages) * (L::kTile8 >> 4));
+                if (leader) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk)
-                        mma_f8(tmem + L::TM_S + g * 128, kdesc<D>(qt + part * kGroupRows * D + kk * 32), kdesc<D>(kt + kk * 32),
-                               kIdS, part + kk > 0);
-                mma_commit(&bars[B_S + g]);
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma_f8(tmem + L::TM_S + g * 128, qd + ((part * kGroupRows * D + kk * 32) >> 4), kd + 2 * kk, kIdS,
+                                   part + kk > 0);
+                    mma_commit(&bars[B_S + g]);
+                }
+                __syncwarp();
             };
-            bool ok = ctl.wait(B_Q, 0) && ctl.wait(B_KF, 0);
+            bool ok = wait(B_Q, 0) && wait(B_KF, 0);
             if (ok) {
                 tc_fence_after();
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
                     if (t_a >= ta[g] && t_a < tb[g]) scores(g, 0);
-                mma_commit(&bars[B_KE]);
+                if (leader) mma_commit(&bars[B_KE]);
+                __syncwarp();
             }
             for (int j = 0; j < nt && ok; ++j) {
-                const int tile = t_a + j, vsl = j % kVStages;
-                ok = ctl.wait(B_CF + vsl, (j / kVStages) & 1);
-                if (ok && j + 1 < nt) ok = ctl.wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1);
+                const int tile = t_a + j, csl = j % kCStages;
+                ok = wait(B_CF + csl, (j / kCStages) & 1) &&
+                     (j + 1 >= nt || wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1));
                 if (!ok) break;
+                const uint64_t vd = dv + csl * (L::kTile16 >> 4);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (tile >= ta[g] && tile < tb[g]) {
-                        ok = ctl.wait(B_P + g, np[g] & 1);
+                        ok = wait(B_P + g, np[g] & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t vt = sb + L::OFF_V + vsl * L::kTile16;
+                        if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < kTok / 16; ++kk)
-                            mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + kk * 8,
-                                       sdesc_sw128(vt + kk * 2048, 16384, 1024), kIdO, np[g] > 0 || kk > 0);
-                        mma_commit(&bars[B_O + g]);
+                            for (int kk = 0; kk < kTok / 16; ++kk)
+                                mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + kk * 8, vd + kk * 128, kIdO,
+                                           np[g] > 0 || kk > 0);
+                            mma_commit(&bars[B_O + g]);
+                        }
+                        __syncwarp();
                         ++np[g];
                     }
+                    // both groups' products with V are issued: its buffer is free when they are done, which the next
+                    // scores need not delay (V is converted a tile ahead into it)
+                    if (g == 1 && leader) mma_commit(&bars[B_CE + csl]);
                     if (j + 1 < nt && tile + 1 >= ta[g] && tile + 1 < tb[g]) {
                         // the scores go where P lies, which the product just issued still reads
-                        if (np[g] > 0) ok = ctl.wait(B_O + g, (np[g] - 1) & 1);
+                        if (np[g] > 0) ok = wait(B_O + g, (np[g] - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         scores(g, j + 1);
                     }
                 }
                 if (!ok) break;
-                mma_commit(&bars[B_CE + vsl]);
-                if (j + 1 < nt) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
+                if (j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
+                __syncwarp();
             }
-            mma_commit(&bars[B_END]);
-            ctl.drain(B_END, 0);
+            if (leader) {
+                mma_commit(&bars[B_END]);
+                ctl.drain(B_END, 0);
+            }
         }
     } else if (warp >= 4 && warp < 8) {
         // ================================================================ V: codes -> fp16, a token a thread
@@ -377,12 +400,12 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         int id_next = block_of(1);
         bool ok = true, nan = false;
         for (int j = 0; j < nt && ok; ++j) {
-            const int sl = j % kVStages;
+            const int sl = j % kVStages, csl = j % kCStages;
             const float s_raw = s_next;
             s_next = scale_of(id_next);
             id_next = block_of(j + 2);
             ok = ctl.wait(B_VF + sl, (j / kVStages) & 1);
-            if (ok && j >= kVStages) ok = ctl.wait(B_CE + sl, (j / kVStages - 1) & 1);
+            if (ok && j >= kCStages) ok = ctl.wait(B_CE + csl, (j / kCStages - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool e = s_raw >= 0.f;
@@ -390,7 +413,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const __half2 f = __float2half2_rn(s);
             __half2 probe = __float2half2_rn(0.f);
             const uint8_t *src = smem + L::OFF_V8 + sl * L::kTile8;
-            uint8_t *dst = smem + L::OFF_V + sl * L::kTile16;
+            uint8_t *dst = smem + L::OFF_V + csl * L::kTile16;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
                 uint4 w = *reinterpret_cast<const uint4 *>(src + kswz<D>(tk, c));
@@ -417,7 +440,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bars[B_CF + sl]);
+                mbar_arrive(&bars[B_CF + csl]);
                 mbar_arrive(&bars[B_VE + sl]);
             }
         }
