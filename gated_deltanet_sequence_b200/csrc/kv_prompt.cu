@@ -5,8 +5,8 @@
 // 128-row UMMA tile, and walks the 128-token tiles of the cache that some row sees:
 //   S = Q K^T   kind::f8f6f4: the cache's codes are the operand as TMA brings them; queries are the sum of
 //               two e4m3 parts (row scaled by a power of two), so two products into one accumulator
-//   P = 2^(S rk - m)   rk: row and block scale; m: a reference that moves only when an exponent passes it
-//               by kSlack, so that the accumulators are rarely rescaled; P as fp16 over S in tensor memory
+//   P = 2^(S rk - m)   rk: row and block scale; m: a reference that moves only when a tile's weights sum past
+//               kMaxSum, so that the accumulators are rarely rescaled; P as fp16 over S in tensor memory
 //   O += P V    kind::f16: V's codes converted to fp16 in shared memory once for both groups, times the
 //               block's scale over the unit's largest (a power of two: exact)
 // Scores cannot be in fp32 here (two e4m3 parts hold a bf16 query exactly down to 2^-9 of its row's largest
@@ -16,7 +16,7 @@
 // exponentials 1024 of the special-function units, so the two groups' softmax and products are interleaved:
 // one group's exponentials run under the other's products.
 //
-// Warps: 0 TMA and block scales, 1 UMMA issue, 2 tensor memory, 4-7 V conversion, 8-11 and 12-15 the groups.
+// Warps: 0 K tiles and scales, 1 UMMA issue, 2 tensor memory, 3 V tiles, 4-7 V conversion, 8-11 and 12-15 the groups.
 // Tensor memory: S (and P over it) of each group, O of each group, 512 columns at d = 128.
 //
 // Two inputs do not fit this scheme, and their request is left to the few-rows kernel, which runs after
@@ -34,26 +34,26 @@ using namespace ptx;
 constexpr int kThreads = 512;
 constexpr int kTok = 128;                 // tokens of a tile
 constexpr int kGroupRows = 128, kUnitRows = 256;
-constexpr int kKStages = 2, kVStages = 2, kCStages = 3, kKsSlots = 8;   // K and V codes, fp16 V, K scales
-constexpr float kSlack = 8.f;
+constexpr int kKStages = 3, kVStages = 3, kCStages = 2, kKsSlots = 8;   // K and V codes, fp16 V, K scales
+constexpr float kMaxSum = 16384.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMinScale = 7.888609052210118e-31f;      // 2^-100: a block of zeros
 constexpr float kSpread = 4096.f;
 
 enum : int {
     B_Q = 0,          // 8 warps: queries written
-    B_KF = 1,         // [2] K tile in
-    B_KE = 3,         // [2] both groups' products with it done
-    B_VF = 5,         // [2] V codes in
-    B_VE = 7,         // [2] converted
-    B_CF = 9,         // [3] fp16 V written
-    B_CE = 12,        // [3] both groups' products with it done
-    B_S = 15,         // [2 groups] scores done
-    B_P = 17,         // [2 groups] weights written, accumulators rescaled
-    B_O = 19,         // [2 groups] P V done
-    B_END = 21,       // everything issued is done
-    B_KS = 22,        // [8] K scales of a tile written
-    kNumBars = 30
+    B_KF = 1,         // [3] K tile in
+    B_KE = 4,         // [3] both groups' products with it done
+    B_VF = 7,         // [3] V codes in
+    B_VE = 10,        // [3] converted
+    B_CF = 13,        // [2] fp16 V written
+    B_CE = 15,        // [2] both groups' products with it done
+    B_S = 17,         // [2 groups] scores done
+    B_P = 19,         // [2 groups] weights written, accumulators rescaled
+    B_O = 21,         // [2 groups] P V done
+    B_END = 23,       // everything issued is done
+    B_KS = 24,        // [8] K scales of a tile written
+    kNumBars = 32
 };
 
 template <int D> struct Lay {
@@ -115,6 +115,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
         : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -257,56 +265,52 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // a warp's wait: most phases are complete when they are looked at, and the abort flag is looked at only in the others
+    auto wait = [&](int b, uint32_t parity) {
+        const bool now = mbar_try_wait(smem_u32(&bars[b]), parity);
+        if (__all_sync(0xffffffffu, now)) return true;
+        return __all_sync(0xffffffffu, ctl.wait(b, parity)) != 0;
+    };
     // The groups keep a row's 128 scores in registers: 256 threads take 192 each, the other 256 64 (65536 in all, what
     // the block was launched with)
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0) {
-        // ================================================================ TMA, K scales
+    if (warp == 0 || warp == 3) {
+        // ================================================================ TMA: K and its scales (warp 0), V (warp 3)
+        const bool is_k = warp == 0;
+        const CUtensorMap *map = is_k ? &mk : &mv;
+        const int full = is_k ? B_KF : B_VF, empty = is_k ? B_KE : B_VE;
+        const uint32_t ring = sb + (is_k ? L::OFF_K : L::OFF_V8);
+        static_assert(kKStages == kVStages, "one ring depth");
         const int bl = a.bs >> 4;                        // 16-token groups of a block
-        int id_next = -1;
         auto look = [&](int j) {                         // block of this lane's 16-token group of tile j
             const int t = (t_a + j) * kTok + 16 * lane;
-            int id = -1;
-            if (lane < 8 && j < nt && t < t_hi) {
-                id = table[t >> a.bs_log2];
-                if (id >= a.num_blocks) id = -1;
-            }
-            return id;
+            const int id = lane < 8 && j < nt && t < t_hi ? table[t >> a.bs_log2] : -1;
+            return id < a.num_blocks ? id : -1;
         };
-        id_next = look(0);
-        int last = -1;
+        int id_next = look(0), last = -1;
         bool ok = true;
         for (int j = 0; j < nt && ok; ++j) {
-            const int id = id_next, t = (t_a + j) * kTok + 16 * lane;
-            const float ks = id >= 0 ? a.k_scale[static_cast<long long>(id) * a.Hkv + h] : 1.f;
+            const int id = id_next, t = (t_a + j) * kTok + 16 * lane, sl = j % kKStages;
+            const float ks = is_k && id >= 0 ? a.k_scale[static_cast<long long>(id) * a.Hkv + h] : 1.f;
             id_next = look(j + 1);
             const bool box = id >= 0 && lane % bl == 0;
             const uint32_t boxes = __ballot_sync(0xffffffffu, box), have = __ballot_sync(0xffffffffu, id >= 0);
-            const uint32_t bytes = __popc(boxes) * a.bs * D;
             const int row = ((id * a.Hkv + h) << a.bs_log2) + (t & (a.bs - 1));
-            const int ksl = j % kKStages, vsl = j % kVStages;
-            if (j >= kKStages) ok = ctl.wait(B_KE + ksl, (j / kKStages - 1) & 1);
-            if (j >= kVStages && ok) ok = ctl.wait(B_VE + vsl, (j / kVStages - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
+            if (j >= kKStages) ok = wait(empty + sl, (j / kKStages - 1) & 1);
             if (!ok) break;
-            if (lane < 8) s_ks[(j % kKsSlots) * 8 + lane] = ks;
-            if (lane == 0) s_have[j % kKsSlots] = have;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[full + sl], __popc(boxes) * a.bs * D);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars[B_KS + j % kKsSlots]);
-                mbar_arrive_expect_tx(&bars[B_KF + ksl], bytes);
-                mbar_arrive_expect_tx(&bars[B_VF + vsl], bytes);
-            }
-            __syncwarp();
-            if (box) {
-                tma_2d(sb + L::OFF_K + ksl * L::kTile8 + 16 * lane * D, &mk, &bars[B_KF + ksl], 0, row);
-                tma_2d(sb + L::OFF_V8 + vsl * L::kTile8 + 16 * lane * D, &mv, &bars[B_VF + vsl], 0, row);
+            if (box) tma_2d(ring + sl * L::kTile8 + 16 * lane * D, map, &bars[full + sl], 0, row);
+            if (is_k) {
+                if (lane < 8) s_ks[(j % kKsSlots) * 8 + lane] = ks;
+                if (lane == 0) s_have[j % kKsSlots] = have;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_KS + j % kKsSlots]);
             }
             last = j;
         }
         // never leave a copy in flight past the end of the block
-        for (int j = max(0, last - kKStages + 1); j <= last; ++j) ctl.drain(B_KF + j % kKStages, (j / kKStages) & 1);
-        for (int j = max(0, last - kVStages + 1); j <= last; ++j) ctl.drain(B_VF + j % kVStages, (j / kVStages) & 1);
+        for (int j = max(0, last - kKStages + 1); j <= last; ++j) ctl.drain(full + j % kKStages, (j / kKStages) & 1);
     } else if (warp == 1) {
         // ================================================================ UMMA issue
         // The whole warp runs the loop and one elected lane issues: in code the compiler knows to be uniform the
@@ -317,7 +321,6 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const bool leader = elect_one();
             const uint64_t dq = kdesc<D>(sb + L::OFF_Q), dk = kdesc<D>(sb + L::OFF_K), dv = sdesc_sw128(sb + L::OFF_V, 16384, 1024);
             int np[2] = {0, 0};                          // P V products issued, by group
-            auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, ctl.wait(b, parity)) != 0; };
             auto scores = [&](int g, int j) {            // S_g = Q_g K_j^T
                 const uint64_t qd = dq + ((g * 2 * kGroupRows * D) >> 4), kd = dk + ((j % kKStages) * (L::kTile8 >> 4));
                 if (leader) {
@@ -377,6 +380,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
                 __syncwarp();
             }
+            __syncwarp();
             if (leader) {
                 mma_commit(&bars[B_END]);
                 ctl.drain(B_END, 0);
@@ -404,9 +408,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const float s_raw = s_next;
             s_next = scale_of(id_next);
             id_next = block_of(j + 2);
-            ok = ctl.wait(B_VF + sl, (j / kVStages) & 1);
-            if (ok && j >= kCStages) ok = ctl.wait(B_CE + csl, (j / kCStages - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait(B_VF + sl, (j / kVStages) & 1);
+            if (ok && j >= kCStages) ok = wait(B_CE + csl, (j / kCStages - 1) & 1);
             if (!ok) break;
             const bool e = s_raw >= 0.f;
             const float s = fmaxf(s_raw, 0.f) * inv_vu;   // exact: powers of two
@@ -511,47 +514,66 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         bool ok = true;
         for (int tile = ta[g]; tile < tb[g] && ok; ++tile, ++done) {
             const int j = tile - t_a, t0 = tile * kTok, slot = j % kKsSlots;
-            ok = ctl.wait(B_KS + slot, (j / kKsSlots) & 1) && ctl.wait(B_S + g, done & 1);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait(B_KS + slot, (j / kKsSlots) & 1) && wait(B_S + g, done & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t have = s_have[slot];
             const bool edge = have != 0xffu || t0 + kTok - 1 > pf[g] || t0 < lo_last;
             const int c_hi = hi - t0, c_lo = lo - t0;    // columns this row sees
-            // the row's 128 scores, and the largest exponent
-            float s[kTok];
+            float s[kTok];                               // the row's 128 scores
+            auto load_scores = [&]() {
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) tmem_ld32(ts + 32 * ch, *reinterpret_cast<float (*)[32]>(s + 32 * ch));
-            tmem_wait_ld();
-            if (edge) {
+                for (int ch = 0; ch < 4; ++ch) tmem_ld32(ts + 32 * ch, *reinterpret_cast<float (*)[32]>(s + 32 * ch));
+                tmem_wait_ld();
+                if (edge) {
 #pragma unroll
-                for (int c = 0; c < kTok; ++c) s[c] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[c] : kNegInf;
-            }
-            float top = kNegInf, k[8];
+                    for (int c = 0; c < kTok; ++c)
+                        s[c] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[c] : kNegInf;
+                }
+            };
+            float k[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                k[q] = rf * s_ks[slot * 8 + q];
-                float x[8];
+            for (int q = 0; q < 8; ++q) k[q] = rf * s_ks[slot * 8 + q];
+            // Weights against the row's reference m. m is the largest exponent of the row's first tile with something to
+            // see, and stays while a tile's weights sum to at most kMaxSum (then none of them is beyond fp16): the
+            // sum is there anyway, so most tiles need no maximum, and their accumulators no rescaling.
+            uint32_t p[kTok / 2];
+            float sum;
+            auto weights = [&]() {
+                const float base = m == kNegInf ? 0.f : m;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * q + i], s[16 * q + 8 + i]);
-#pragma unroll
-                for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-                    for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
-                if (x[0] > kNegInf) top = fmaxf(top, x[0] * k[q]);
-            }
+                for (int c = 0; c < kTok; c += 2) {
+                    const float x = ex2(fmaf(s[c], k[c >> 4], -base)), y = ex2(fmaf(s[c + 1], k[c >> 4], -base));
+                    part[(c >> 1) & 3] += x + y;
+                    p[c >> 1] = pack_h2(x, y);
+                }
+                sum = (part[0] + part[1]) + (part[2] + part[3]);
+            };
             const bool none = m == kNegInf;
-            const bool move = none ? top > kNegInf : top > m + kSlack;
-            if (__any_sync(0xffffffffu, move)) {
-                float f = 1.f;
-                if (move) {
+            load_scores();
+            weights();
+            if (__any_sync(0xffffffffu, (none && in) || sum > kMaxSum)) {
+                load_scores();                           // (not kept: the weights take their registers)
+                float top = kNegInf, f = 1.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * q + i], s[16 * q + 8 + i]);
+#pragma unroll
+                    for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+                        for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
+                    if (x[0] > kNegInf) top = fmaxf(top, x[0] * k[q]);
+                }
+                if (top > m) {
                     f = none ? 0.f : ex2(m - top);
                     m = top;
                     l *= f;
                 }
                 if (done > 0) {                          // rescale the row's accumulators: P V before this must be done
-                    ok = ctl.wait(B_O + g, (done - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = wait(B_O + g, (done - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -564,29 +586,17 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         tmem_st16(to + 16 * ch, o);
                     }
                 }
+                weights();
             }
-            const float base = m == kNegInf ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                float p[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const int c = 32 * ch + i;
-                    const float x = ex2(fmaf(s[c], k[c >> 4], -base)), y = ex2(fmaf(s[c + 1], k[c >> 4], -base));
-                    sum[(i >> 1) & 3] += x + y;
-                    p[i >> 1] = __uint_as_float(pack_h2(x, y));
-                }
-                tmem_st16(ts + 16 * ch, p);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            for (int ch = 0; ch < 4; ++ch) tmem_st16u(ts + 16 * ch, p + 16 * ch);
+            l += sum;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_P + g]);
         }
-        if (ok && done > 0) ok = ctl.wait(B_O + g, (done - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
+        if (ok && done > 0) ok = wait(B_O + g, (done - 1) & 1);
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : vu / l;
         __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + (token * a.Hq + head) * D;
