@@ -32,7 +32,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 512;
-constexpr int kTok = 128;                 // tokens of a tile
+constexpr int kTok = 128, kHalf = 64;     // tokens of a tile; scores and weights go half by half
 constexpr int kGroupRows = 128, kUnitRows = 256;
 constexpr int kKStages = 3, kVStages = 3, kCStages = 2, kKsSlots = 8;   // K and V codes, fp16 V, K scales
 constexpr float kMaxSum = 16384.f;
@@ -48,12 +48,12 @@ enum : int {
     B_VE = 10,        // [3] converted
     B_CF = 13,        // [2] fp16 V written
     B_CE = 15,        // [2] both groups' products with it done
-    B_S = 17,         // [2 groups] scores done
-    B_P = 19,         // [2 groups] weights written, accumulators rescaled
-    B_O = 21,         // [2 groups] P V done
-    B_END = 23,       // everything issued is done
-    B_KS = 24,        // [8] K scales of a tile written
-    kNumBars = 32
+    B_S = 17,         // [2 groups][2 halves] scores done
+    B_P = 21,         // [2 groups][2 halves] weights written, accumulators rescaled
+    B_O = 25,         // [2 groups][2 halves] P V done
+    B_END = 29,       // everything issued is done
+    B_KS = 30,        // [8] K scales of a tile written
+    kNumBars = 38
 };
 
 template <int D> struct Lay {
@@ -116,6 +116,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
 }
+// Wait for this thread's tensor-memory loads; the values are tied to it, so that no use is moved before it.
+__device__ __forceinline__ void tmem_wait_ld32(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                   "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                   "+f"(r[30]), "+f"(r[31])::"memory");
+}
+// Two fp32 values in a register pair, and Blackwell's two-wide fp32 instructions on them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -148,21 +175,67 @@ __device__ __forceinline__ void e4m3_to_h2(uint32_t w, __half2 &lo, __half2 &hi)
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 
-// The request and row tile (of 256 rows) with index `idx` among those of this kernel, last tiles (the longest) first.
+// The request and row tile (of 256 rows) that block `idx` takes: tiles in falling order of the kv tile they end in, so
+// that the longest units start first whatever the requests' lengths are, and the last blocks to run are the shortest
+// (by request, the SMs that got one unit more than others took 15 % longer than the mean). A request's row tiles end
+// later and later, so those that end in kv tile E or later are its last ones, counted in closed form; E is found by
+// bisection over all requests.
 struct Unit {
     int n, rt;
 };
+struct Rows {
+    int rows, tiles, p0;     // rows (0: not for this kernel), row tiles, position of the first row
+};
+__device__ __forceinline__ Rows unit_rows(const AttnArgs &a, int n) {
+    const ReqWork w = request_work(a, n, true);
+    const int rows = w.many ? w.qlen * (a.Hq / a.Hkv) : 0;
+    return Rows{rows, (rows + kUnitRows - 1) / kUnitRows, w.kv - w.qlen};
+}
+// first row tile of the request that ends in kv tile e or later (rows.tiles: none)
+__device__ __forceinline__ int first_from(const Rows &q, int e, int G) {
+    const long long need = static_cast<long long>(G) * (static_cast<long long>(e) * kTok - q.p0);     // last row >= need
+    if (need <= 0) return 0;
+    const long long t = (need + kUnitRows) / kUnitRows - 1;
+    if (t < q.tiles - 1) return static_cast<int>(t);
+    return q.rows - 1 >= need ? max(q.tiles - 1, 0) : q.tiles;
+}
 __device__ __forceinline__ bool find_unit(const AttnArgs &a, int idx, Unit *out) {
+    __shared__ int s_part[2][kThreads / 32];
     __shared__ int s_sum[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
     const int per = (a.N + kThreads - 1) / kThreads;
     const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
-    auto tiles = [&](int n) {
-        const ReqWork w = request_work(a, n, true);
-        return w.many ? static_cast<int>((static_cast<long long>(w.qlen) * G + kUnitRows - 1) / kUnitRows) : 0;
+    const Rows first = n0 < n1 ? unit_rows(a, n0) : Rows{0, 0, 0};
+    int turn = 0;
+    auto block_sum = [&](int x) {
+        const int w = __reduce_add_sync(0xffffffffu, x);
+        if (lane == 0) s_part[turn][warp] = w;
+        __syncthreads();
+        int t = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) t += s_part[turn][i];
+        turn ^= 1;
+        return t;
     };
-    int own = 0;
-    for (int n = n0; n < n1; ++n) own += tiles(n);
+    auto own_from = [&](int e) {         // this thread's row tiles that end in kv tile e or later
+        int c = 0;
+        for (int n = n0; n < n1; ++n) {
+            const Rows q = n == n0 ? first : unit_rows(a, n);
+            c += q.tiles - first_from(q, e, G);
+        }
+        return c;
+    };
+    if (tid == 0) out->n = -1;
+    // the largest e with more than idx tiles from it on (rows before position 0 end "in" tile 0)
+    int lo = 0, hi = a.max_blocks * a.bs / kTok + 1;
+    if (block_sum(own_from(0)) <= idx) return false;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (block_sum(own_from(mid)) > idx) lo = mid;
+        else hi = mid;
+    }
+    const int after = block_sum(own_from(lo + 1));
+    const int own = own_from(lo) - own_from(lo + 1);
     int inc = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -170,22 +243,25 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int idx, Unit *out)
         if (lane >= off) inc += y;
     }
     if (lane == 31) s_sum[warp] = inc;
-    if (tid == 0) out->n = -1;
     __syncthreads();
-    int before = inc - own, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_sum[w];
-        total += s_sum[w];
-    }
-    const int at = total - 1 - idx;
+    int before = inc - own;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    const int at = idx - after;
     if (at >= before && at < before + own) {
-        int n = n0, b = before;
-        for (int c = tiles(n); at >= b + c; c = tiles(n)) { b += c; ++n; }
-        out->n = n;
-        out->rt = at - b;
+        int b = before;
+        for (int n = n0; n < n1; ++n) {
+            const Rows q = unit_rows(a, n);
+            const int f = first_from(q, lo, G), c = first_from(q, lo + 1, G) - f;
+            if (at < b + c) {
+                out->n = n;
+                out->rt = f + (at - b);
+                break;
+            }
+            b += c;
+        }
     }
     __syncthreads();
-    return at >= 0;
+    return true;
 }
 
 template <int D>
@@ -317,20 +393,22 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // descriptors live in uniform registers (issued by a lane of a divergent branch, an instruction took 130
         // cycles for the pipe's 65).
         if (nt > 0) {
-            constexpr uint32_t kIdS = idesc_e4m3(128, kTok), kIdO = idesc_f16(128, D, false, true);
+            constexpr uint32_t kIdS = idesc_e4m3(128, kHalf), kIdO = idesc_f16(128, D, false, true);
             const bool leader = elect_one();
             const uint64_t dq = kdesc<D>(sb + L::OFF_Q), dk = kdesc<D>(sb + L::OFF_K), dv = sdesc_sw128(sb + L::OFF_V, 16384, 1024);
-            int np[2] = {0, 0};                          // P V products issued, by group
-            auto scores = [&](int g, int j) {            // S_g = Q_g K_j^T
-                const uint64_t qd = dq + ((g * 2 * kGroupRows * D) >> 4), kd = dk + ((j % kKStages) * (L::kTile8 >> 4));
+            int np[2] = {0, 0};                          // tiles of each group so far
+            auto active = [&](int g, int j) { return j < nt && t_a + j >= ta[g] && t_a + j < tb[g]; };
+            auto scores = [&](int g, int j, int hf) {    // S_g[hf] = Q_g K_j[hf]^T
+                const uint64_t qd = dq + ((g * 2 * kGroupRows * D) >> 4);
+                const uint64_t kd = dk + (j % kKStages) * (L::kTile8 >> 4) + ((hf * kHalf * D) >> 4);
                 if (leader) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk)
-                            mma_f8(tmem + L::TM_S + g * 128, qd + ((part * kGroupRows * D + kk * 32) >> 4), kd + 2 * kk, kIdS,
-                                   part + kk > 0);
-                    mma_commit(&bars[B_S + g]);
+                            mma_f8(tmem + L::TM_S + g * 128 + hf * kHalf, qd + ((part * kGroupRows * D + kk * 32) >> 4),
+                                   kd + 2 * kk, kIdS, part + kk > 0);
+                    mma_commit(&bars[B_S + 2 * g + hf]);
                 }
                 __syncwarp();
             };
@@ -338,47 +416,50 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (ok) {
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    if (t_a >= ta[g] && t_a < tb[g]) scores(g, 0);
+                for (int i = 0; i < 4; ++i)
+                    if (active(i & 1, 0)) scores(i & 1, 0, i >> 1);
                 if (leader) mma_commit(&bars[B_KE]);
                 __syncwarp();
             }
+            // Half by half: P V of both groups, then the scores that take the same half of the next tile. These wait for the
+            // P V just issued, which reads the weights in their place; meanwhile the groups work on the other half,
+            // whose scores are there since the turn before.
             for (int j = 0; j < nt && ok; ++j) {
-                const int tile = t_a + j, csl = j % kCStages;
-                ok = wait(B_CF + csl, (j / kCStages) & 1) &&
-                     (j + 1 >= nt || wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1));
-                if (!ok) break;
+                const int csl = j % kCStages;
+                ok = wait(B_CF + csl, (j / kCStages) & 1);
                 const uint64_t vd = dv + csl * (L::kTile16 >> 4);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (tile >= ta[g] && tile < tb[g]) {
-                        ok = wait(B_P + g, np[g] & 1);
-                        if (!ok) break;
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!ok || !active(g, j)) continue;
+                        ok = wait(B_P + 2 * g + hf, np[g] & 1);
+                        if (!ok) continue;
                         tc_fence_after();
                         if (leader) {
 #pragma unroll
-                            for (int kk = 0; kk < kTok / 16; ++kk)
-                                mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + kk * 8, vd + kk * 128, kIdO,
-                                           np[g] > 0 || kk > 0);
-                            mma_commit(&bars[B_O + g]);
+                            for (int kk = 0; kk < kHalf / 16; ++kk)
+                                mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + hf * kHalf + kk * 8,
+                                           vd + (hf * (kHalf / 16) + kk) * 128, kIdO, np[g] > 0 || hf > 0 || kk > 0);
+                            mma_commit(&bars[B_O + 2 * g + hf]);
                         }
                         __syncwarp();
-                        ++np[g];
                     }
-                    // both groups' products with V are issued: its buffer is free when they are done, which the next
-                    // scores need not delay (V is converted a tile ahead into it)
-                    if (g == 1 && leader) mma_commit(&bars[B_CE + csl]);
-                    if (j + 1 < nt && tile + 1 >= ta[g] && tile + 1 < tb[g]) {
-                        // the scores go where P lies, which the product just issued still reads
-                        if (np[g] > 0) ok = wait(B_O + g, (np[g] - 1) & 1);
-                        if (!ok) break;
+                    if (ok && hf == 1 && leader) mma_commit(&bars[B_CE + csl]);      // every product with V is issued
+                    if (ok && hf == 0 && j + 1 < nt) ok = wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!ok || !active(g, j + 1)) continue;
+                        if (active(g, j)) ok = wait(B_O + 2 * g + hf, np[g] & 1);
+                        if (!ok) continue;
                         tc_fence_after();
-                        scores(g, j + 1);
+                        scores(g, j + 1, hf);
                     }
                 }
-                if (!ok) break;
-                if (j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
+                if (ok && j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
                 __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) np[g] += active(g, j) ? 1 : 0;
             }
             __syncwarp();
             if (leader) {
@@ -512,68 +593,81 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         float m = kNegInf, l = 0.f;
         int done = 0;                                    // tiles of this group so far
         bool ok = true;
-        for (int tile = ta[g]; tile < tb[g] && ok; ++tile, ++done) {
-            const int j = tile - t_a, t0 = tile * kTok, slot = j % kKsSlots;
-            ok = wait(B_KS + slot, (j / kKsSlots) & 1) && wait(B_S + g, done & 1);
+        for (int i = 2 * ta[g]; i < 2 * tb[g] && ok; ++i) {              // half tiles
+            const int tile = i >> 1, hf = i & 1, j = tile - t_a, t0 = i * kHalf, slot = j % kKsSlots;
+            done = tile - ta[g];
+            ok = wait(B_KS + slot, (j / kKsSlots) & 1) && wait(B_S + 2 * g + hf, done & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t have = s_have[slot];
-            const bool edge = have != 0xffu || t0 + kTok - 1 > pf[g] || t0 < lo_last;
+            const uint32_t have = (s_have[slot] >> (4 * hf)) & 0xfu, tsh = ts + hf * kHalf;
+            const bool edge = have != 0xfu || t0 + kHalf - 1 > pf[g] || t0 < lo_last;
             const int c_hi = hi - t0, c_lo = lo - t0;    // columns this row sees
-            float s[kTok];                               // the row's 128 scores
-            auto load_scores = [&]() {
+            float k[4];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) tmem_ld32(ts + 32 * ch, *reinterpret_cast<float (*)[32]>(s + 32 * ch));
-                tmem_wait_ld();
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < kTok; ++c)
-                        s[c] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[c] : kNegInf;
-                }
-            };
-            float k[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) k[q] = rf * s_ks[slot * 8 + q];
-            // Weights against the row's reference m. m is the largest exponent of the row's first tile with something to
-            // see, and stays while a tile's weights sum to at most kMaxSum (then none of them is beyond fp16): the
-            // sum is there anyway, so most tiles need no maximum, and their accumulators no rescaling.
-            uint32_t p[kTok / 2];
+            for (int q = 0; q < 4; ++q) k[q] = rf * s_ks[slot * 8 + 4 * hf + q];
+            // Weights against the row's reference m. m is the largest exponent of the row's first half tile with something
+            // to see, and stays while a half tile's weights sum to at most kMaxSum (then none of them is beyond
+            // fp16): the sum is there anyway, so most half tiles need no maximum, and their accumulators no rescaling.
+            uint32_t p[kHalf / 2];
             float sum;
-            auto weights = [&]() {
-                const float base = m == kNegInf ? 0.f : m;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+            auto mask = [&](float (&s)[32], int ch) {
 #pragma unroll
-                for (int c = 0; c < kTok; c += 2) {
-                    const float x = ex2(fmaf(s[c], k[c >> 4], -base)), y = ex2(fmaf(s[c + 1], k[c >> 4], -base));
-                    part[(c >> 1) & 3] += x + y;
-                    p[c >> 1] = pack_h2(x, y);
+                for (int c = 32 * ch; c < 32 * ch + 32; ++c)
+                    s[c & 31] = c <= c_hi && c >= c_lo && ((have >> (c >> 4)) & 1u) ? s[c & 31] : kNegInf;
+            };
+            auto weights = [&]() {                       // 32 scores at a time, the next 32 on their way
+                const float base = m == kNegInf ? 0.f : m;
+                float s[2][32];
+                uint64_t part[2] = {0, 0};               // two running sums each
+                tmem_ld32(tsh, s[0]);
+#pragma unroll
+                for (int ch = 0; ch < kHalf / 32; ++ch) {
+                    float(&cur)[32] = s[ch & 1];
+                    tmem_wait_ld32(cur);
+                    if (ch < kHalf / 32 - 1) tmem_ld32(tsh + 32 * (ch + 1), s[(ch + 1) & 1]);
+                    if (edge) mask(cur, ch);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float kk = k[2 * ch + (c >> 4)];
+                        const uint64_t x = fma2(pair(cur[c], cur[c + 1]), pair(kk, kk), pair(-base, -base));
+                        const uint64_t e = pair(ex2(lo2(x)), ex2(hi2(x)));
+                        part[(c >> 1) & 1] = add2(part[(c >> 1) & 1], e);
+                        p[16 * ch + (c >> 1)] = pack_h2(lo2(e), hi2(e));
+                    }
                 }
-                sum = (part[0] + part[1]) + (part[2] + part[3]);
+                const uint64_t t = add2(part[0], part[1]);
+                sum = lo2(t) + hi2(t);
             };
             const bool none = m == kNegInf;
-            load_scores();
             weights();
             if (__any_sync(0xffffffffu, (none && in) || sum > kMaxSum)) {
-                load_scores();                           // (not kept: the weights take their registers)
                 float top = kNegInf, f = 1.f;
+#pragma unroll 1
+                for (int ch = 0; ch < kHalf / 32; ++ch) {
+                    float s[32];
+                    tmem_ld32(tsh + 32 * ch, s);
+                    tmem_wait_ld32(s);
+                    if (edge) mask(s, ch);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float x[8];
+                    for (int q = 0; q < 2; ++q) {
+                        float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaxf(s[16 * q + i], s[16 * q + 8 + i]);
+                        for (int c = 0; c < 8; ++c) x[c] = fmaxf(s[16 * q + c], s[16 * q + 8 + c]);
 #pragma unroll
-                    for (int w = 4; w >= 1; w >>= 1)
+                        for (int w = 4; w >= 1; w >>= 1)
 #pragma unroll
-                        for (int i = 0; i < w; ++i) x[i] = fmaxf(x[i], x[i + w]);
-                    if (x[0] > kNegInf) top = fmaxf(top, x[0] * k[q]);
+                            for (int c = 0; c < w; ++c) x[c] = fmaxf(x[c], x[c + w]);
+                        if (x[0] > kNegInf) top = fmaxf(top, x[0] * (rf * s_ks[slot * 8 + 4 * hf + 2 * ch + q]));
+                    }
                 }
                 if (top > m) {
                     f = none ? 0.f : ex2(m - top);
                     m = top;
                     l *= f;
                 }
-                if (done > 0) {                          // rescale the row's accumulators: P V before this must be done
-                    ok = wait(B_O + g, (done - 1) & 1);
+                if (i > 2 * ta[g]) {                     // rescale the row's accumulators: P V before this must be done
+                    const int b = i - 1;
+                    ok = wait(B_O + 2 * g + (b & 1), ((b >> 1) - ta[g]) & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -582,21 +676,22 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         tmem_ld16(to + 16 * ch, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                        for (int c = 0; c < 16; ++c) o[c] *= f;
                         tmem_st16(to + 16 * ch, o);
                     }
                 }
                 weights();
             }
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) tmem_st16u(ts + 16 * ch, p + 16 * ch);
+            tmem_st16u(tsh, p);
+            tmem_st16u(tsh + 16, p + 16);
             l += sum;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_P + g]);
+            if (lane == 0) mbar_arrive(&bars[B_P + 2 * g + hf]);
         }
-        if (ok && done > 0) ok = wait(B_O + g, (done - 1) & 1);
+        done = tb[g] - ta[g];
+        if (ok && done > 0) ok = wait(B_O + 2 * g + 1, (done - 1) & 1);
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : vu / l;
         __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + (token * a.Hq + head) * D;
