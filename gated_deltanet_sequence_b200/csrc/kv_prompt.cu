@@ -16,7 +16,7 @@
 // exponentials 1024 of the special-function units, so the two groups' softmax and products are interleaved:
 // one group's exponentials run under the other's products.
 //
-// Warps: 0 K tiles and scales, 1 UMMA issue, 2 tensor memory, 3 V tiles, 4-7 V conversion, 8-11 and 12-15 the groups.
+// Warps: 0 K tiles and scales, 1-2 UMMA issue (2: tensor memory too), 3 V tiles, 4-7 V conversion, 8-11 and 12-15 the groups.
 // Tensor memory: S (and P over it) of each group, O of each group, 512 columns at d = 128.
 //
 // Two inputs do not fit this scheme, and their request is left to the few-rows kernel, which runs after
@@ -51,9 +51,10 @@ enum : int {
     B_S = 17,         // [2 groups][2 halves] scores done
     B_P = 21,         // [2 groups][2 halves] weights written, accumulators rescaled
     B_O = 25,         // [2 groups][2 halves] P V done
-    B_END = 29,       // everything issued is done
-    B_KS = 30,        // [8] K scales of a tile written
-    kNumBars = 38
+    B_END = 29,       // [2 groups] everything issued is done
+    B_KS = 31,        // [8] K scales of a tile written
+    B_VU = 39,        // V's unit known
+    kNumBars = 40
 };
 
 template <int D> struct Lay {
@@ -199,69 +200,48 @@ __device__ __forceinline__ int first_from(const Rows &q, int e, int G) {
     if (t < q.tiles - 1) return static_cast<int>(t);
     return q.rows - 1 >= need ? max(q.tiles - 1, 0) : q.tiles;
 }
+// Every warp finds it for itself (no barrier); lane i looks at requests i, i + 32, ...
 __device__ __forceinline__ bool find_unit(const AttnArgs &a, int idx, Unit *out) {
-    __shared__ int s_part[2][kThreads / 32];
-    __shared__ int s_sum[kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
-    const int per = (a.N + kThreads - 1) / kThreads;
-    const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
-    const Rows first = n0 < n1 ? unit_rows(a, n0) : Rows{0, 0, 0};
-    int turn = 0;
-    auto block_sum = [&](int x) {
-        const int w = __reduce_add_sync(0xffffffffu, x);
-        if (lane == 0) s_part[turn][warp] = w;
-        __syncthreads();
-        int t = 0;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) t += s_part[turn][i];
-        turn ^= 1;
-        return t;
-    };
-    auto own_from = [&](int e) {         // this thread's row tiles that end in kv tile e or later
-        int c = 0;
-        for (int n = n0; n < n1; ++n) {
-            const Rows q = n == n0 ? first : unit_rows(a, n);
+    const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+    const Rows none{0, 0, 0};
+    const Rows q0 = lane < a.N ? unit_rows(a, lane) : none, q1 = lane + 32 < a.N ? unit_rows(a, lane + 32) : none;
+    auto req = [&](int n) { return n == lane ? q0 : n == lane + 32 ? q1 : n < a.N ? unit_rows(a, n) : none; };
+    auto from = [&](int e) {             // row tiles that end in kv tile e or later
+        int c = (q0.tiles - first_from(q0, e, G)) + (q1.tiles - first_from(q1, e, G));
+        for (int n = lane + 64; n < a.N; n += 32) {
+            const Rows q = unit_rows(a, n);
             c += q.tiles - first_from(q, e, G);
         }
-        return c;
+        return __reduce_add_sync(0xffffffffu, c);
     };
-    if (tid == 0) out->n = -1;
     // the largest e with more than idx tiles from it on (rows before position 0 end "in" tile 0)
     int lo = 0, hi = a.max_blocks * a.bs / kTok + 1;
-    if (block_sum(own_from(0)) <= idx) return false;
+    if (from(0) <= idx) return false;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (block_sum(own_from(mid)) > idx) lo = mid;
+        if (from(mid) > idx) lo = mid;
         else hi = mid;
     }
-    const int after = block_sum(own_from(lo + 1));
-    const int own = own_from(lo) - own_from(lo + 1);
-    int inc = own;
+    int at = idx - from(lo + 1);         // among those that end in kv tile lo, in request order
+    for (int base = 0; base < a.N; base += 32) {
+        const Rows q = req(base + lane);
+        const int f = first_from(q, lo, G), own = first_from(q, lo + 1, G) - f;
+        int inc = own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += y;
-    }
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    int before = inc - own;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    const int at = idx - after;
-    if (at >= before && at < before + own) {
-        int b = before;
-        for (int n = n0; n < n1; ++n) {
-            const Rows q = unit_rows(a, n);
-            const int f = first_from(q, lo, G), c = first_from(q, lo + 1, G) - f;
-            if (at < b + c) {
-                out->n = n;
-                out->rt = f + (at - b);
-                break;
-            }
-            b += c;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
         }
+        const uint32_t hit = __ballot_sync(0xffffffffu, at < inc);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            out->n = base + src;
+            out->rt = __shfl_sync(0xffffffffu, f + at - (inc - own), src);
+            return true;
+        }
+        at -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    __syncthreads();
-    return true;
+    return false;
 }
 
 template <int D>
@@ -277,24 +257,24 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     float *s_ks = reinterpret_cast<float *>(smem + L::OFF_KS);                       // [slot][8]
     uint32_t *s_have = reinterpret_cast<uint32_t *>(s_ks + kKsSlots * 8);            // [slot]
-    __shared__ Unit s_unit;
-    __shared__ unsigned s_vmax, s_vmin;
+    __shared__ float s_vrange[4][2], s_vu;
     const Ctl ctl{bars, abort_flag, a.err, a.wait_limit};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv, h = blockIdx.x % a.Hkv;
 
     if (tid == 0) {
         for (int b = 0; b < kNumBars; ++b)
-            mbar_init(&bars[b], b == B_Q ? 8 : (b >= B_VE && b < B_CE) || (b >= B_P && b < B_O) ? 4 : 1);
+            mbar_init(&bars[b], b == B_Q                                                          ? 8
+                                : (b >= B_VE && b < B_CE) || (b >= B_P && b < B_O)                ? 4
+                                : (b >= B_KE && b < B_VF) || (b >= B_CE && b < B_S)               ? 2
+                                                                                                  : 1);
         *abort_flag = 0;
-        s_vmax = __float_as_uint(kMinScale);
-        s_vmin = 0x7f800000u;
         fence_mbar_init();
         prefetch_tmap(&mk);
         prefetch_tmap(&mv);
     }
-    if (!find_unit(a, blockIdx.x / a.Hkv, &s_unit)) return;
-    const Unit u = s_unit;
+    Unit u{};
+    if (!find_unit(a, blockIdx.x / a.Hkv, &u)) return;
     const ReqWork rw = request_work(a, u.n, true);
     const int rows = rw.qlen * G, p0 = rw.kv - rw.qlen;
     // positions of each group's first and last row, and its tiles
@@ -313,26 +293,6 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int t_hi = max(pl[0], pl[1]) + 1;
     const int *table = a.table + static_cast<long long>(u.n) * a.max_blocks;
 
-    // V's largest scale here, and the smallest of a block that is not all zeros
-    {
-        float mx = kMinScale, mn = __int_as_float(0x7f800000);
-        const int b1 = (t_hi + a.bs - 1) >> a.bs_log2;
-        for (int b = ((t_a * kTok) >> a.bs_log2) + tid; b < b1; b += kThreads) {
-            const int id = table[b];
-            if (id < 0 || id >= a.num_blocks) { atomicOr(a.err, kErrBadSeqlens); continue; }
-            const float s = a.v_scale[static_cast<long long>(id) * a.Hkv + h];
-            mx = fmaxf(mx, s);
-            if (s > kMinScale) mn = fminf(mn, s);
-        }
-        atomicMax(&s_vmax, __float_as_uint(mx));
-        atomicMin(&s_vmin, __float_as_uint(mn));
-    }
-    __syncthreads();
-    const float vu = __uint_as_float(s_vmax);
-    if (vu > kSpread * __uint_as_float(s_vmin)) {         // fp16 would lose the smaller blocks
-        if (tid == 0) redo[u.n] = 1;
-        return;
-    }
     if (warp == 2) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -387,85 +347,69 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
         // never leave a copy in flight past the end of the block
         for (int j = max(0, last - kKStages + 1); j <= last; ++j) ctl.drain(full + j % kKStages, (j / kKStages) & 1);
-    } else if (warp == 1) {
-        // ================================================================ UMMA issue
+    } else if (warp < 3) {
+        // ================================================================ UMMA issue, a warp for each group
         // The whole warp runs the loop and one elected lane issues: in code the compiler knows to be uniform the
         // descriptors live in uniform registers (issued by a lane of a divergent branch, an instruction took 130
-        // cycles for the pipe's 65).
-        if (nt > 0) {
-            constexpr uint32_t kIdS = idesc_e4m3(128, kHalf), kIdO = idesc_f16(128, D, false, true);
-            const bool leader = elect_one();
-            const uint64_t dq = kdesc<D>(sb + L::OFF_Q), dk = kdesc<D>(sb + L::OFF_K), dv = sdesc_sw128(sb + L::OFF_V, 16384, 1024);
-            int np[2] = {0, 0};                          // tiles of each group so far
-            auto active = [&](int g, int j) { return j < nt && t_a + j >= ta[g] && t_a + j < tb[g]; };
-            auto scores = [&](int g, int j, int hf) {    // S_g[hf] = Q_g K_j[hf]^T
-                const uint64_t qd = dq + ((g * 2 * kGroupRows * D) >> 4);
-                const uint64_t kd = dk + (j % kKStages) * (L::kTile8 >> 4) + ((hf * kHalf * D) >> 4);
-                if (leader) {
+        // cycles for the pipe's 65). A wait costs a warp about 200 cycles even when there is nothing to wait for; with
+        // a warp for each group, one group's products run meanwhile.
+        const int g = warp - 1;
+        constexpr uint32_t kIdS = idesc_e4m3(128, kHalf), kIdO = idesc_f16(128, D, false, true);
+        const bool leader = elect_one();
+        const uint32_t tsg = tmem + L::TM_S + g * 128, tog = tmem + L::TM_O + g * D;
+        const uint64_t dq = kdesc<D>(sb + L::OFF_Q + g * 2 * kGroupRows * D), dk = kdesc<D>(sb + L::OFF_K);
+        const uint64_t dv = sdesc_sw128(sb + L::OFF_V, 16384, 1024);
+        const int j0 = ta[g] - t_a, j1 = tb[g] - t_a;    // this group's tiles
+        auto scores = [&](int j, int hf) {               // S[hf] = Q K_j[hf]^T
+            const uint64_t kd = dk + (j % kKStages) * (L::kTile8 >> 4) + ((hf * kHalf * D) >> 4);
+            if (leader) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk)
-                            mma_f8(tmem + L::TM_S + g * 128 + hf * kHalf, qd + ((part * kGroupRows * D + kk * 32) >> 4),
-                                   kd + 2 * kk, kIdS, part + kk > 0);
-                    mma_commit(&bars[B_S + 2 * g + hf]);
-                }
-                __syncwarp();
-            };
-            bool ok = wait(B_Q, 0) && wait(B_KF, 0);
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (active(i & 1, 0)) scores(i & 1, 0, i >> 1);
-                if (leader) mma_commit(&bars[B_KE]);
-                __syncwarp();
-            }
-            // Half by half: P V of both groups, then the scores that take the same half of the next tile. These wait for the
-            // P V just issued, which reads the weights in their place; meanwhile the groups work on the other half,
-            // whose scores are there since the turn before.
-            for (int j = 0; j < nt && ok; ++j) {
-                const int csl = j % kCStages;
-                ok = wait(B_CF + csl, (j / kCStages) & 1);
-                const uint64_t vd = dv + csl * (L::kTile16 >> 4);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (!ok || !active(g, j)) continue;
-                        ok = wait(B_P + 2 * g + hf, np[g] & 1);
-                        if (!ok) continue;
-                        tc_fence_after();
-                        if (leader) {
-#pragma unroll
-                            for (int kk = 0; kk < kHalf / 16; ++kk)
-                                mma_f16_ts(tmem + L::TM_O + g * D, tmem + L::TM_S + g * 128 + hf * kHalf + kk * 8,
-                                           vd + (hf * (kHalf / 16) + kk) * 128, kIdO, np[g] > 0 || hf > 0 || kk > 0);
-                            mma_commit(&bars[B_O + 2 * g + hf]);
-                        }
-                        __syncwarp();
-                    }
-                    if (ok && hf == 1 && leader) mma_commit(&bars[B_CE + csl]);      // every product with V is issued
-                    if (ok && hf == 0 && j + 1 < nt) ok = wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (!ok || !active(g, j + 1)) continue;
-                        if (active(g, j)) ok = wait(B_O + 2 * g + hf, np[g] & 1);
-                        if (!ok) continue;
-                        tc_fence_after();
-                        scores(g, j + 1, hf);
-                    }
-                }
-                if (ok && j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);
-                __syncwarp();
-#pragma unroll
-                for (int g = 0; g < 2; ++g) np[g] += active(g, j) ? 1 : 0;
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_f8(tsg + hf * kHalf, dq + ((part * kGroupRows * D + kk * 32) >> 4), kd + 2 * kk, kIdS, part + kk > 0);
+                mma_commit(&bars[B_S + 2 * g + hf]);
             }
             __syncwarp();
-            if (leader) {
-                mma_commit(&bars[B_END]);
-                ctl.drain(B_END, 0);
+        };
+        bool ok = nt > 0 && wait(B_Q, 0);
+        // Tile by tile and half by half: P V, then the scores that take the same half of the next tile. These wait for the P V
+        // just issued, which reads the weights in their place; meanwhile the group works on the other half.
+        for (int j = -1; j < nt && ok; ++j) {
+            const bool pv = j >= j0 && j < j1, qk = j + 1 >= j0 && j + 1 < j1;
+            const int par = (j - j0) & 1;
+            if (j >= 0) ok = wait(B_CF + j % kCStages, (j / kCStages) & 1);
+            if (ok && j + 1 < nt) ok = wait(B_KF + (j + 1) % kKStages, ((j + 1) / kKStages) & 1);
+            const uint64_t vd = dv + (j % kCStages) * (L::kTile16 >> 4);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                if (pv && ok) {
+                    ok = wait(B_P + 2 * g + hf, par);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_f16_ts(tog, tsg + hf * kHalf + kk * 8, vd + (hf * (kHalf / 16) + kk) * 128, kIdO,
+                                       j > j0 || hf > 0 || kk > 0);
+                        mma_commit(&bars[B_O + 2 * g + hf]);
+                    }
+                    __syncwarp();
+                }
+                if (hf == 1 && ok && j >= 0 && leader) mma_commit(&bars[B_CE + j % kCStages]);   // through with V
+                if (qk && ok) {
+                    if (pv) ok = wait(B_O + 2 * g + hf, par);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(j + 1, hf);
+                }
             }
+            if (ok && j + 1 < nt && leader) mma_commit(&bars[B_KE + (j + 1) % kKStages]);        // through with K
+            __syncwarp();
+        }
+        if (leader) {
+            mma_commit(&bars[B_END + g]);
+            ctl.drain(B_END + g, 0);
         }
     } else if (warp >= 4 && warp < 8) {
         // ================================================================ V: codes -> fp16, a token a thread
@@ -480,6 +424,34 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         auto scale_of = [&](int id) {
             return id >= 0 && id < a.num_blocks ? a.v_scale[static_cast<long long>(id) * a.Hkv + h] : -1.f;
         };
+        // V's largest scale here is the unit that V is converted in; the smallest of a block that is not all zeros has to
+        // be within kSpread of it, or fp16 would lose it
+        float vu;
+        {
+            float mx = kMinScale, mn = __int_as_float(0x7f800000);
+            const int b1 = (t_hi + a.bs - 1) >> a.bs_log2;
+            for (int b = ((t_a * kTok) >> a.bs_log2) + tk; b < b1; b += 128) {
+                const int id = table[b];
+                if (id < 0 || id >= a.num_blocks) { atomicOr(a.err, kErrBadSeqlens); continue; }
+                const float s = a.v_scale[static_cast<long long>(id) * a.Hkv + h];
+                mx = fmaxf(mx, s);
+                if (s > kMinScale) mn = fminf(mn, s);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+            }
+            if (lane == 0) { s_vrange[warp - 4][0] = mx; s_vrange[warp - 4][1] = mn; }
+            named_bar(1, 128);
+            vu = fmaxf(fmaxf(s_vrange[0][0], s_vrange[1][0]), fmaxf(s_vrange[2][0], s_vrange[3][0]));
+            mn = fminf(fminf(s_vrange[0][1], s_vrange[1][1]), fminf(s_vrange[2][1], s_vrange[3][1]));
+            if (tk == 0) {
+                if (vu > kSpread * mn) redo[u.n] = 1;
+                s_vu = vu;
+                mbar_arrive(&bars[B_VU]);
+            }
+        }
         const float inv_vu = 1.f / vu;
         float s_next = scale_of(block_of(0));             // negative: the token does not exist
         int id_next = block_of(1);
@@ -693,7 +665,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         done = tb[g] - ta[g];
         if (ok && done > 0) ok = wait(B_O + 2 * g + 1, (done - 1) & 1);
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : vu / l;
+        ok = ok && wait(B_VU, 0);
+        const float inv = l == 0.f ? 0.f : s_vu / l;
         __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + (token * a.Hq + head) * D;
         if (ok) {
 #pragma unroll
