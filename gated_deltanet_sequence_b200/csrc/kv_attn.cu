@@ -57,8 +57,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 }
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -92,8 +91,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, long l
 }
 // the same for an e4m3 query: D += A (16 x 32, e4m3) B (32 x 8, e4m3)
 __device__ __forceinline__ void mma16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -132,7 +130,8 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t h) {      // 0xffff in t
 enum QKind { kF8, kF16, kF16x2 };
 
 // A warp's row state while a unit runs, and its steps.
-template <int D, QKind QK, bool PSPLIT>
+// HV: block scales of a step (2 where blocks hold 16 tokens)
+template <int D, QKind QK, bool PSPLIT, int HV>
 struct Worker {
     static constexpr int KS = QK == kF8 ? D / 32 : D / 16;     // k-steps of Q K^T
     static constexpr int NT = D / 8;                           // n-tiles of P V
@@ -205,34 +204,42 @@ struct Worker {
     // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's two
     // halves; EDGE: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
     template <bool EDGE>
-    __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[2], const float (&vs)[2],
+    __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[HV], const float (&vs)[HV],
                                          uint32_t tok) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        // (the four token groups side by side: a group's own products are a chain)
         float x[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + token_of(g);
-            x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+        for (int j = 0; j < 4; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                const int swz = D == 128 ? (r & 7) : ((r >> 1) & 3);
-                uint32_t w[4];
+        for (int half = 0; half < D / 64; ++half) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 8 * j + token_of(g), swz = D == 128 ? (r & 7) : ((r >> 1) & 3);
                 asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "=r"(w[j][0]), "=r"(w[j][1]), "=r"(w[j][2]), "=r"(w[j][3])
                              : "r"(sk + r * D + (((c + 4 * half) ^ swz) << 4)));
-                if constexpr (QK == kF8) {
+            }
+            if constexpr (QK == kF8) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        mma16832(x[j], qa[2 * half + i], w[2 * i], w[2 * i + 1]);
-                        mma16832(x[j], ql[2 * half + i], w[2 * i], w[2 * i + 1]);
-                    }
-                } else {
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t b0, b1;
-                        e4m3_to_h2(w[i], b0, b1);
-                        mma16816(x[j], qa[4 * half + i], b0, b1);
-                        if constexpr (QK == kF16x2) mma16816(x[j], ql[4 * half + i], b0, b1);
+                    for (int j = 0; j < 4; ++j) mma16832(x[j], qa[2 * half + i], w[j][2 * i], w[j][2 * i + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma16832(x[j], ql[2 * half + i], w[j][2 * i], w[j][2 * i + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t b0[4], b1[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e4m3_to_h2(w[j][i], b0[j], b1[j]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma16816(x[j], qa[4 * half + i], b0[j], b1[j]);
+                    if constexpr (QK == kF16x2) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma16816(x[j], ql[4 * half + i], b0[j], b1[j]);
                     }
                 }
             }
@@ -248,12 +255,17 @@ struct Worker {
         float top = kNegInf;
         {
             const float base[2] = {none[0] ? 0.f : m[0], none[1] ? 0.f : m[1]};
-            const float rk[2][2] = {{rf[0] * ks[0], rf[1] * ks[0]}, {rf[0] * ks[1], rf[1] * ks[1]}};
+            float rk[HV][2];
+#pragma unroll
+            for (int b = 0; b < HV; ++b) {
+                rk[b][0] = rf[0] * ks[b];
+                rk[b][1] = rf[1] * ks[b];
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[j][i] = fmaf(x[j][i], rk[j >> 1][i >> 1], -base[i >> 1]);
+                    x[j][i] = fmaf(x[j][i], rk[HV == 1 ? 0 : j >> 1][i >> 1], -base[i >> 1]);
                     if (EDGE) x[j][i] = sees(j, i) ? x[j][i] : kNegInf;
                     top = fmaxf(top, x[j][i]);
                 }
@@ -287,10 +299,10 @@ struct Worker {
             }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
-            if (vs[hf] != vu) {
-                const float u = vu == 0.f ? 1.f : vu / vs[hf];
+            if (hf < HV && vs[hf < HV ? hf : 0] != vu) {
+                const float u = vu == 0.f ? 1.f : vu / vs[hf < HV ? hf : 0];
                 scale_o(u, u);
-                vu = vs[hf];
+                vu = vs[hf < HV ? hf : 0];
             }
             uint32_t p[4], pl[4];
             float(&xa)[4] = x[2 * hf], (&xb)[4] = x[2 * hf + 1];
@@ -382,11 +394,11 @@ struct Worker {
     }
 };
 
-template <int D, QKind QK, bool PSPLIT, typename IT>
+template <int D, QKind QK, bool PSPLIT, int HV, typename IT>
 __global__ void __launch_bounds__(kThreads, Smem<D>::kBlocks)
 kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
     using S = Smem<D>;
-    using W = Worker<D, QK, PSPLIT>;
+    using W = Worker<D, QK, PSPLIT, HV>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t s_bar[kWarps][S::kStages];
     __shared__ Share s_share;
@@ -409,28 +421,28 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
     const uint32_t ring = smem_u32(smem) + warp * S::kRing;
     uint32_t phase = 0;                     // parity bit of each stage
-    const int br = min(a.bs, kStep), nb = kStep / br;       // rows of a TMA box; boxes of a step
+    constexpr int br = kStep / HV;          // rows of a TMA box
 
     int n = sh.n;
     long long off = sh.off, left = sh.end - sh.begin;
     bool first_unit = true;
+    ReqWork rw = request_work(a, n);
     while (left > 0) {
-        const ReqWork rw = request_work(a, n);
         if (off >= rw.work) {
             off -= rw.work;
-            ++n;
+            rw = request_work(a, ++n);
             continue;
         }
         // the unit (head, row tile) and its part of this share
         const int cost = rw.tiles + kUnitCost;
-        const long long unit = off / cost;
-        const int at = static_cast<int>(off - unit * cost);
+        const int unit = static_cast<int>(off < 0x7fffffff ? static_cast<unsigned>(off) / static_cast<unsigned>(cost) : off / cost);
+        const int at = static_cast<int>(off - static_cast<long long>(unit) * cost);
         const int take = static_cast<int>(min(left, static_cast<long long>(cost - at)));
         const int tile0 = max(0, at - kUnitCost), ntile = max(0, at + take - kUnitCost) - tile0;
         off += take;
         left -= take;
         if (ntile == 0) continue;           // the share ends before the unit's first tile
-        const int h = static_cast<int>(unit / rw.row_tiles), rt = static_cast<int>(unit - static_cast<long long>(h) * rw.row_tiles);
+        const int h = unit / rw.row_tiles, rt = unit - h * rw.row_tiles;
         const int rows = rw.qlen * G;
         const int p_first = rw.kv - rw.qlen + rt * kRows / G;
         const int p_last = rw.kv - rw.qlen + min(rt * kRows + kRows - 1, rows - 1) / G;
@@ -442,16 +454,16 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         const int *table = a.table + static_cast<long long>(n) * a.max_blocks;
         // block numbers and scales of the warp's next 32 steps, one step a lane
         struct Bank {
-            int blk[2];
-            float ksc[2], vsc[2];
+            int blk[HV];
+            float ksc[HV], vsc[HV];
         } cur, nxt;
         auto fetch_blocks = [&](Bank &bank, int step0) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < HV; ++b) {
                 const int t = t_lo + (step0 + lane) * kTile + warp * kStep + b * br;
                 bank.blk[b] = -1;
                 bank.ksc[b] = bank.vsc[b] = 1.f;
-                if (b < nb && t < t_hi) {
+                if (t < t_hi) {
                     const int id = table[t >> a.bs_log2];
                     if (id >= 0 && id < a.num_blocks) {
                         bank.blk[b] = id;
@@ -463,36 +475,33 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 }
             }
         };
-        auto issue = [&](int i, const Bank &bank) {           // copies of step i
-            const int st = i % S::kStages, t = t_lo + i * kTile + warp * kStep;
-            const int b0 = __shfl_sync(0xffffffffu, bank.blk[0], i & 31);
-            const int b1 = __shfl_sync(0xffffffffu, bank.blk[1], i & 31);
-            const int boxes = (b0 >= 0) + (nb > 1 && b1 >= 0);
+        auto issue = [&](int i, int stage, const Bank &bank) {           // copies of step i
+            const int t = t_lo + i * kTile + warp * kStep;
+            int id[HV], boxes = 0;
+#pragma unroll
+            for (int b = 0; b < HV; ++b) {
+                id[b] = __shfl_sync(0xffffffffu, bank.blk[b], i & 31);
+                boxes += id[b] >= 0 ? 1 : 0;
+            }
             if (lane == 0 && boxes > 0) {
-                uint64_t *bar = &s_bar[warp][st];
-                const uint32_t dst = ring + st * S::kStageBytes;
+                uint64_t *bar = &s_bar[warp][stage];
                 mbar_arrive_expect_tx(bar, 2 * boxes * br * D);
-                const int r0 = t & (a.bs - 1);
-                if (b0 >= 0) {
-                    tma_load_2d(dst, &mk, bar, 0, ((b0 * a.Hkv + h) << a.bs_log2) + r0);
-                    tma_load_2d(dst + S::kStepBytes, &mv, bar, 0, ((b0 * a.Hkv + h) << a.bs_log2) + r0);
-                }
-                if (nb > 1 && b1 >= 0) {
-                    tma_load_2d(dst + br * D, &mk, bar, 0, (b1 * a.Hkv + h) << a.bs_log2);
-                    tma_load_2d(dst + S::kStepBytes + br * D, &mv, bar, 0, (b1 * a.Hkv + h) << a.bs_log2);
-                }
+#pragma unroll
+                for (int b = 0; b < HV; ++b)
+                    if (id[b] >= 0) {
+                        const uint32_t dst = ring + stage * S::kStageBytes + b * br * D;
+                        const int row = ((id[b] * a.Hkv + h) << a.bs_log2) + (HV == 1 ? t & (a.bs - 1) : 0);
+                        tma_load_2d(dst, &mk, bar, 0, row);
+                        tma_load_2d(dst + S::kStepBytes, &mv, bar, 0, row);
+                    }
             }
             return boxes > 0;
         };
         // steps of this warp: those that start before t_hi
         const int nstep = t_hi > t_lo + warp * kStep ? (t_hi - t_lo - warp * kStep + kTile - 1) / kTile : 0;
-        fetch_blocks(cur, 0);
-        nxt = cur;
-        uint32_t live = 0;                  // steps in flight that have copies, by stage
-        for (int i = 0; i < min(nstep, S::kStages - 1); ++i)
-            if (issue(i, cur)) live |= 1u << (i % S::kStages);
-
-        // queries, in fragment order: k-step 4 half + i, coordinates 16 (c + 4 half) + 4 i + 0 .. 3
+        // queries, in fragment order: coordinates 16 (c + 4 half) + 4 i + 0 .. 3 of rows g and g + 8. Their loads go out
+        // before the block numbers' and are used after the first copies are under way.
+        float qf[2][D / 4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int R = rt * kRows + g + 8 * r;
@@ -500,47 +509,59 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             const int tok = R / G;
             const IT *qp = static_cast<const IT *>(a.q) + (rw.row0 + tok) * a.q_stride +
                            static_cast<long long>(h * G + (R - tok * G)) * D;
-            float f[D / 4];
 #pragma unroll
             for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) load4(in ? qp + 16 * (c + 4 * half) + 4 * i : nullptr, &f[16 * half + 4 * i]);
-            w.set_query(r, f, a.scale_log2);
+                for (int i = 0; i < 4; ++i) load4(in ? qp + 16 * (c + 4 * half) + 4 * i : nullptr, &qf[r][16 * half + 4 * i]);
             w.hi[r] = in ? rw.kv - rw.qlen + tok : -1;
             w.lo[r] = a.window > 0 ? w.hi[r] - a.window + 1 : 0;
             w.m[r] = kNegInf;
             w.l[r] = 0.f;
         }
+        fetch_blocks(cur, 0);
+        nxt = cur;
+        uint32_t live = 0;                  // steps in flight that have copies, by stage
+        for (int i = 0; i < min(nstep, S::kStages - 1); ++i)
+            if (issue(i, i, cur)) live |= 1u << i;
+
+#pragma unroll
+        for (int r = 0; r < 2; ++r) w.set_query(r, qf[r], a.scale_log2);
 #pragma unroll
         for (int i = 0; i < W::NT; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
         w.vu = 0.f;
 
         const int lo_last = a.window > 0 ? p_last - a.window + 1 : 0;
         bool ok = true;
-        for (int i = 0; i < nstep; ++i) {
-            const int st = i % S::kStages, t = t_lo + i * kTile + warp * kStep;
+        struct Step {
+            int t;
+            float ks[HV], vs[HV];
+            uint32_t tok;          // tokens that exist
+            bool edge;             // some row does not see some token
+        };
+        auto look = [&](int i) {
+            Step x;
+            x.t = t_lo + i * kTile + warp * kStep;
             if ((i & 31) == 0 && i > 0) cur = nxt;
             if ((i & 31) == 8 && i + 24 < nstep) fetch_blocks(nxt, i + 24);
-            const int b0 = __shfl_sync(0xffffffffu, cur.blk[0], i & 31);
-            const int b1 = __shfl_sync(0xffffffffu, cur.blk[1], i & 31);
-            float ks[2], vs[2];
-            ks[0] = __shfl_sync(0xffffffffu, cur.ksc[0], i & 31);
-            vs[0] = __shfl_sync(0xffffffffu, cur.vsc[0], i & 31);
-            ks[1] = ks[0];
-            vs[1] = vs[0];
-            uint32_t tok = b0 >= 0 ? 0xffffffffu : 0u;
-            if (nb > 1) {
-                ks[1] = __shfl_sync(0xffffffffu, cur.ksc[1], i & 31);
-                vs[1] = __shfl_sync(0xffffffffu, cur.vsc[1], i & 31);
-                tok = (b0 >= 0 ? 0xffffu : 0u) | (b1 >= 0 ? 0xffff0000u : 0u);
+            x.tok = 0u;
+#pragma unroll
+            for (int b = 0; b < HV; ++b) {
+                x.ks[b] = __shfl_sync(0xffffffffu, cur.ksc[b], i & 31);
+                x.vs[b] = __shfl_sync(0xffffffffu, cur.vsc[b], i & 31);
+                const int id = __shfl_sync(0xffffffffu, cur.blk[b], i & 31);
+                if (id >= 0) x.tok |= (HV == 1 ? 0xffffffffu : 0xffffu) << (16 * b);
             }
-            if (t_hi - t < kStep) tok &= (1u << (t_hi - t)) - 1u;
-            // the ring: the next step's copies go out before this one is waited for
+            if (t_hi - x.t < kStep) x.tok &= (1u << (t_hi - x.t)) - 1u;
+            x.edge = x.tok != 0xffffffffu || x.t + kStep - 1 > p_first || x.t < lo_last;
+            return x;
+        };
+        int st = 0, nst = (S::kStages - 1) % S::kStages;      // stages of step i and of the one sent out beside it
+        auto turn = [&](int i) {            // sends a later step's copies out, waits for this one's
             __syncwarp();
             const int nx = i + S::kStages - 1;
             if (nx < nstep && ok) {
-                const uint32_t bit = 1u << (nx % S::kStages);
-                live = issue(nx, (nx >> 5) == (i >> 5) ? cur : nxt) ? live | bit : live & ~bit;
+                const uint32_t bit = 1u << nst;
+                live = issue(nx, nst, (nx >> 5) == (i >> 5) ? cur : nxt) ? live | bit : live & ~bit;
             }
             if (ok && (live & (1u << st))) {
                 const uint32_t par = (phase >> st) & 1u;
@@ -554,10 +575,25 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 phase ^= 1u << st;
             }
             const uint32_t sk = ring + st * S::kStageBytes;
-            const bool edge = tok != 0xffffffffu || t + kStep - 1 > p_first || t < lo_last;
-            if (ok && tok != 0u) {
-                if (edge) w.template step<true>(sk, sk + S::kStepBytes, t, ks, vs, tok);
-                else w.template step<false>(sk, sk + S::kStepBytes, t, ks, vs, tok);
+            nst = st;
+            st = st + 1 == S::kStages ? 0 : st + 1;
+            return sk;
+        };
+        // Runs of steps of one kind, each in a loop of its own: with both kinds in one loop the accumulators changed
+        // registers at every turn (300 moves a step).
+        int i = 0;
+        Step nx;
+        if (nstep > 0) nx = look(0);
+        while (i < nstep) {
+            while (i < nstep && !nx.edge) {
+                const uint32_t sk = turn(i);
+                if (ok) w.template step<false>(sk, sk + S::kStepBytes, nx.t, nx.ks, nx.vs, nx.tok);
+                if (++i < nstep) nx = look(i);
+            }
+            while (i < nstep && nx.edge) {
+                const uint32_t sk = turn(i);
+                if (ok && nx.tok != 0u) w.template step<true>(sk, sk + S::kStepBytes, nx.t, nx.ks, nx.vs, nx.tok);
+                if (++i < nstep) nx = look(i);
             }
         }
 
@@ -592,32 +628,33 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         // a block leaves at most two parts: the end of a unit begun by another block (slot 0), and the start
         // of one that another ends (slot 1; a middle piece goes to slot 0)
         float *part = whole ? nullptr : a.ws + (2ll * blockIdx.x + (first_unit && tile0 > 0 ? 0 : 1)) * part_floats(D);
-        constexpr int TPR = kThreads / kRows;               // threads of a row
-        constexpr int CPT = D / TPR;                        // columns of a thread
-        const int r = tid / TPR, x = (tid % TPR) * CPT;
-        float mm = kNegInf;
+        // a row at a time to a warp (two at d = 64), four columns a lane
+        constexpr int RPW = 128 / D, LPR = 32 / RPW;
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) mm = fmaxf(mm, s_ml[q][r][0]);
-        const float base = mm == kNegInf ? 0.f : mm;
-        float ll = 0.f, acc[CPT];
+        for (int q = 0; q < kRows / (kWarps * RPW); ++q) {
+            const int r = (q * kWarps + warp) * RPW + lane / LPR, x = (lane % LPR) * 4;
+            float mm = kNegInf;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) acc[i] = 0.f;
+            for (int p = 0; p < kWarps; ++p) mm = fmaxf(mm, s_ml[p][r][0]);
+            const float base = mm == kNegInf ? 0.f : mm;
+            float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) {
-            const float f = ex2(s_ml[q][r][0] - base);
-            ll = fmaf(s_ml[q][r][1], f, ll);
-#pragma unroll
-            for (int i = 0; i < CPT; ++i) acc[i] = fmaf(mg[(q * kRows + r) * S::kMergeRow + x + i], f, acc[i]);
-        }
-        const int R = rt * kRows + r;
-        if (whole) {
-            if (R < rows) store_row<CPT>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
-        } else {
-            if (x == 0) { part[r] = mm; part[kRows + r] = ll; }
-#pragma unroll
-            for (int i = 0; i < CPT; i += 4)
-                *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + x + i) =
-                    make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            for (int p = 0; p < kWarps; ++p) {
+                const float f = ex2(s_ml[p][r][0] - base);
+                const float4 v = *reinterpret_cast<const float4 *>(mg + (p * kRows + r) * S::kMergeRow + x);
+                ll = fmaf(s_ml[p][r][1], f, ll);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                acc[2] = fmaf(v.z, f, acc[2]);
+                acc[3] = fmaf(v.w, f, acc[3]);
+            }
+            const int R = rt * kRows + r;
+            if (whole) {
+                if (R < rows) store_row<4>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
+            } else {
+                if (x == 0) { part[r] = mm; part[kRows + r] = ll; }
+                *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + x) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            }
         }
         if (tile0 == 0 && ntile < rw.tiles)      // begun here, ended in a later share
             cut = CutUnit{rw.row0, h, rt, min(kRows, rows - rt * kRows),
@@ -685,7 +722,7 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinWarps) kv_attn_join_kern
 
 template <int D, QKind QK, bool PSPLIT, typename IT>
 gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
-    auto kern = kv_attn_kernel<D, QK, PSPLIT, IT>;
+    auto kern = a.bs == 16 ? kv_attn_kernel<D, QK, PSPLIT, 2, IT> : kv_attn_kernel<D, QK, PSPLIT, 1, IT>;
     if (!ensure_smem_limit(reinterpret_cast<const void *>(kern), Smem<D>::kBytes)) return GDN_ERR_CUDA;
     kern<<<grid, kThreads, Smem<D>::kBytes, stream>>>(mk, mv, a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
