@@ -201,6 +201,15 @@ struct Worker {
         }
     }
 
+    __device__ __forceinline__ void no_query(int r) {
+        rf[r] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qa[s][r] = qa[s][r + 2] = 0u;
+            if constexpr (QK != kF16) ql[s][r] = ql[s][r + 2] = 0u;
+        }
+    }
+
     // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's two
     // halves; EDGE: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
     template <bool EDGE>
@@ -524,8 +533,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         for (int i = 0; i < min(nstep, S::kStages - 1); ++i)
             if (issue(i, i, cur)) live |= 1u << i;
 
-#pragma unroll
-        for (int r = 0; r < 2; ++r) w.set_query(r, qf[r], a.scale_log2);
+        const int nrows = min(kRows, rows - rt * kRows);        // rows of this tile
+        w.set_query(0, qf[0], a.scale_log2);
+        if (nrows > 8) w.set_query(1, qf[1], a.scale_log2);
+        else w.no_query(1);
 #pragma unroll
         for (int i = 0; i < W::NT; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
         w.vu = 0.f;
@@ -611,6 +622,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         float *mg = reinterpret_cast<float *>(smem);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+            if (g + 8 * r >= nrows) break;
             float *row = mg + (warp * kRows + g + 8 * r) * S::kMergeRow;
             // n-tile i: column 2c is coordinate x0 + i, column 2c + 1 coordinate x1 + i
             const int x0 = 16 * c, x1 = D == 128 ? 64 + 16 * c : 16 * c + 8;
@@ -633,6 +645,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
         for (int q = 0; q < kRows / (kWarps * RPW); ++q) {
             const int r = (q * kWarps + warp) * RPW + lane / LPR, x = (lane % LPR) * 4;
+            if (r >= nrows) break;
             float mm = kNegInf;
 #pragma unroll
             for (int p = 0; p < kWarps; ++p) mm = fmaxf(mm, s_ml[p][r][0]);
@@ -650,14 +663,14 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             const int R = rt * kRows + r;
             if (whole) {
-                if (R < rows) store_row<4>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
+                store_row<4>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
             } else {
                 if (x == 0) { part[r] = mm; part[kRows + r] = ll; }
                 *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + x) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             }
         }
         if (tile0 == 0 && ntile < rw.tiles)      // begun here, ended in a later share
-            cut = CutUnit{rw.row0, h, rt, min(kRows, rows - rt * kRows),
+            cut = CutUnit{rw.row0, h, rt, nrows,
                           static_cast<int>((sh.end + rw.tiles - ntile - 1) / sh.per) - static_cast<int>(blockIdx.x) + 1};
         // the rings take copies again: what was read and written through the generic proxy comes before them
         fence_proxy_async();
