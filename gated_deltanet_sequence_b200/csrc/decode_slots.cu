@@ -35,7 +35,7 @@ struct SlotArgs {
 };
 
 template <int DK, int DV, typename IT, bool DELTA>
-__global__ void __launch_bounds__(kSlotThreads)
+__global__ void __launch_bounds__(kSlotThreads, DK * DV == 16384 ? 2 : DK * DV == 8192 ? 3 : 4)
 decode_slots_kernel(const IT *__restrict__ q, const IT *__restrict__ k, const IT *__restrict__ v, const SlotArgs a,
                     unsigned *__restrict__ err) {
     constexpr int CG = DV / 4, RG = kSlotThreads / CG, RPT = DK / RG;

@@ -30,7 +30,8 @@ struct AppArgs {
     uint8_t *cache[2];
     float *scale[2];
     const int *slot;
-    int T, H, bs_log2, num_blocks, R;
+    int T, H, bs_log2, num_blocks;
+    int R, HG;                 // rows and heads of a block
 };
 
 // 8 values (one chunk) of a row, as fp32
@@ -133,20 +134,22 @@ __device__ __forceinline__ void rescale_codes(uint8_t *p, int bytes, float ratio
     }
 }
 
-template <int D, typename IT>
-__global__ void __launch_bounds__(kAppThreads)
+// MB: the largest block size (64 or 128): a thread holds MB * D / 8 / 256 chunks of a long run, twice (the next item's
+// values are on their way while one is reduced and coded).
+template <int D, int MB, typename IT>
+__global__ void __launch_bounds__(kAppThreads, (MB == 64 && sizeof(IT) == 2 ? 4 : 2))
 kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
     constexpr int CPR = D / 8;                           // chunks a row
-    constexpr int STEPS = kMaxBs * CPR / kAppThreads;    // chunks a thread of a block's longest run
+    constexpr int STEPS = MB * CPR / kAppThreads;        // chunks a thread of a block's longest run
     __shared__ int s_slot[kMaxRows + kMaxBs];
     __shared__ uint32_t s_brk[kMaskWords];
     __shared__ int s_long[kMaxRows], s_short[kMaxRows], s_nlong, s_nshort;
-    __shared__ float s_max[kAppWarps];
+    __shared__ float s_max[2][kAppWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.y, z = blockIdx.z, bs = 1 << a.bs_log2;
+    const int h0 = blockIdx.y * a.HG, nh = min(a.HG, a.H - h0), z = blockIdx.z, bs = 1 << a.bs_log2;
     const long long r0 = static_cast<long long>(blockIdx.x) * a.R;
     const int nslots = a.num_blocks << a.bs_log2;
-    const IT *x = static_cast<const IT *>(z ? a.x[1] : a.x[0]) + h * D;
+    const IT *x = static_cast<const IT *>(z ? a.x[1] : a.x[0]);
     const long long stride = z ? a.stride[1] : a.stride[0];
     uint8_t *cache = z ? a.cache[1] : a.cache[0];
     float *scale = z ? a.scale[1] : a.scale[0];
@@ -163,7 +166,7 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
             s = a.slot[r];
             if (r > 0) prev = a.slot[r - 1];
             if (s < -1 || s >= nslots) {
-                if (i < a.R && h == 0 && z == 0) atomicOr(err, kErrBadSeqlens);
+                if (i < a.R && h0 == 0 && z == 0) atomicOr(err, kErrBadSeqlens);
                 s = -1;
             }
         }
@@ -186,59 +189,64 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
     }
     __syncthreads();
 
-    // ---- long runs: the whole block
-    const int nlong = s_nlong, nshort = s_nshort;
-    for (int e = 0; e < nlong; ++e) {
-        const int i0 = s_long[e] & 255, len = s_long[e] >> 8;
-        const int slot = s_slot[i0], off = slot & (bs - 1);
-        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h;
-        const float old = scale[bh];
-        Chunk<IT> c[STEPS];
-        float m = 0.f;
+    // ---- long runs, head by head: the whole block
+    const int nlong = s_nlong * nh, nshort = s_nshort * nh;
+    auto load_long = [&](int e, Chunk<IT> (&c)[STEPS]) {
+        const int run = s_long[e / nh], i0 = run & 255, len = run >> 8;
+        const IT *row = x + (r0 + i0 + tid / CPR) * stride + (h0 + e % nh) * D + (tid % CPR) * 8;
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {
-            const int id = tid + j * kAppThreads;
-            if (id < len * CPR) c[j].load(x + (r0 + i0 + id / CPR) * stride + (id % CPR) * 8);
+            if (tid / CPR + j * (kAppThreads / CPR) < len) c[j].load(row + j * (kAppThreads / CPR) * stride);
             else c[j].zero();
         }
+    };
+    Chunk<IT> c[STEPS], ahead[STEPS];
+    if (nlong > 0) load_long(0, ahead);
+    for (int e = 0; e < nlong; ++e) {
+        const int run = s_long[e / nh], i0 = run & 255, len = run >> 8;
+        const int slot = s_slot[i0], off = slot & (bs - 1);
+        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h0 + e % nh;
+        const float old = off > 0 ? scale[bh] : 0.f;
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) c[j] = ahead[j];
+        if (e + 1 < nlong) load_long(e + 1, ahead);
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) m = fmaxf(m, chunk_max(c[j]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) s_max[warp] = m;
-        __syncthreads();
-        m = s_max[0];
+        if (lane == 0) s_max[e & 1][warp] = m;
+        __syncthreads();      // (and the item before is through with the other s_max)
+        m = s_max[e & 1][0];
 #pragma unroll
-        for (int w = 1; w < kAppWarps; ++w) m = fmaxf(m, s_max[w]);
+        for (int w = 1; w < kAppWarps; ++w) m = fmaxf(m, s_max[e & 1][w]);
         const float sc = run_scale(m, off == 0, old);
         const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
         uint8_t *dst = cache + (bh << a.bs_log2) * D;
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-            const int id = tid + j * kAppThreads;
-            if (id < len * CPR) store_codes(dst + off * D + id * 8, c[j], inv);
-        }
+        for (int j = 0; j < STEPS; ++j)
+            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(dst + off * D + (tid + j * kAppThreads) * 8, c[j], inv);
         if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, tid, kAppThreads);
-        __syncthreads();      // everyone has read the old scale and s_max
+        // everyone has read the old scale: each did before the barrier above
         if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     }
 
-    // ---- short runs: one to a warp
+    // ---- short runs: one, of one head, to a warp
     for (int e = warp; e < nshort; e += kAppWarps) {
-        const int i0 = s_short[e] & 255, len = s_short[e] >> 8;
-        const int slot = s_slot[i0], off = slot & (bs - 1);
+        const int run = s_short[e / nh], i0 = run & 255, len = run >> 8;
+        const int slot = s_slot[i0], off = slot & (bs - 1), h = h0 + e % nh;
         const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h;
         const float old = off > 0 ? scale[bh] : 0.f;
-        Chunk<IT> c[kWarpSteps];
+        Chunk<IT> w[kWarpSteps];
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < kWarpSteps; ++j) {
             const int id = lane + j * 32;
-            if (id < len * CPR) c[j].load(x + (r0 + i0 + id / CPR) * stride + (id % CPR) * 8);
-            else c[j].zero();
+            if (id < len * CPR) w[j].load(x + (r0 + i0 + id / CPR) * stride + h * D + (id % CPR) * 8);
+            else w[j].zero();
         }
 #pragma unroll
-        for (int j = 0; j < kWarpSteps; ++j) m = fmaxf(m, chunk_max(c[j]));
+        for (int j = 0; j < kWarpSteps; ++j) m = fmaxf(m, chunk_max(w[j]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float sc = run_scale(m, off == 0, old);
@@ -247,12 +255,18 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
 #pragma unroll
         for (int j = 0; j < kWarpSteps; ++j) {
             const int id = lane + j * 32;
-            if (id < len * CPR) store_codes(dst + off * D + id * 8, c[j], inv);
+            if (id < len * CPR) store_codes(dst + off * D + id * 8, w[j], inv);
         }
         if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, lane, 32);
         __syncwarp();
         if (lane == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     }
+}
+
+template <int D, typename IT>
+void launch_app(const AppArgs &a, dim3 grid, unsigned *err, cudaStream_t stream) {
+    if (a.bs_log2 <= 6) kv_append_kernel<D, 64, IT><<<grid, kAppThreads, 0, stream>>>(a, err);
+    else kv_append_kernel<D, 128, IT><<<grid, kAppThreads, 0, stream>>>(a, err);
 }
 
 }  // namespace
@@ -265,15 +279,18 @@ gdn_status_t launch_kv_append(const void *k, const void *v, long long ks, long l
     int lg = 0;
     while ((1 << lg) < block_size) ++lg;
     AppArgs a{{k, v}, {ks, vs}, {static_cast<uint8_t *>(kc), static_cast<uint8_t *>(vc)}, {ksc, vsc}, slot, T, H, lg,
-              num_blocks, 0};
+              num_blocks, 0, 0};
+    // Prompts: 64 rows and four heads a block, whose items follow each other without a pause. Few rows: 8 rows and one
+    // head, for more blocks.
     a.R = T >= 4096 ? kMaxRows : kAppWarps;
-    const dim3 grid(static_cast<unsigned>((T + a.R - 1) / a.R), static_cast<unsigned>(H), 2);
+    a.HG = T >= 4096 ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>((T + a.R - 1) / a.R), static_cast<unsigned>((H + a.HG - 1) / a.HG), 2);
     if (in_dtype == GDN_F32) {
-        if (d == 128) kv_append_kernel<128, float><<<grid, kAppThreads, 0, stream>>>(a, err);
-        else kv_append_kernel<64, float><<<grid, kAppThreads, 0, stream>>>(a, err);
+        if (d == 128) launch_app<128, float>(a, grid, err, stream);
+        else launch_app<64, float>(a, grid, err, stream);
     } else {
-        if (d == 128) kv_append_kernel<128, __nv_bfloat16><<<grid, kAppThreads, 0, stream>>>(a, err);
-        else kv_append_kernel<64, __nv_bfloat16><<<grid, kAppThreads, 0, stream>>>(a, err);
+        if (d == 128) launch_app<128, __nv_bfloat16>(a, grid, err, stream);
+        else launch_app<64, __nv_bfloat16>(a, grid, err, stream);
     }
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -446,7 +446,15 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         const int cost = rw.tiles + kUnitCost;
         const int unit = static_cast<int>(off < 0x7fffffff ? static_cast<unsigned>(off) / static_cast<unsigned>(cost) : off / cost);
         const int at = static_cast<int>(off - static_cast<long long>(unit) * cost);
-        const int take = static_cast<int>(min(left, static_cast<long long>(cost - at)));
+        int take = static_cast<int>(min(left, static_cast<long long>(cost - at)));
+        if (a.whole) {                      // a share takes the units that start in it, to their ends
+            if (at > 0) {
+                off += take;
+                left -= take;
+                continue;
+            }
+            take = cost;
+        }
         const int tile0 = max(0, at - kUnitCost), ntile = max(0, at + take - kUnitCost) - tile0;
         off += take;
         left -= take;
@@ -739,6 +747,7 @@ gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnAr
     if (!ensure_smem_limit(reinterpret_cast<const void *>(kern), Smem<D>::kBytes)) return GDN_ERR_CUDA;
     kern<<<grid, kThreads, Smem<D>::kBytes, stream>>>(mk, mv, a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (a.whole) return GDN_OK;            // nothing to join
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / kJoinRows);
     cfg.blockDim = dim3(32 * kJoinRows * kJoinWarps);
@@ -792,6 +801,7 @@ size_t kv_attn_ws_bytes(int N, int d) {
 gdn_status_t launch_kv_prompt(const void *kc, const void *vc, const AttnArgs &a, int d, int *redo, cudaStream_t stream);
 
 constexpr int kManyRows = 64;
+constexpr int kWholeTokens = 1024;
 
 gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, bool in_f32, bool out_f32,
                             cudaStream_t stream) {
@@ -804,6 +814,11 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
         return GDN_ERR_CUDA;
     const int grid = kv_attn_grid(d);
     a.cuts = reinterpret_cast<CutUnit *>(a.ws + grid * 2 * part_floats(d));
+    // Contexts (or windows) that the table bounds to this many tokens are not cut
+    const long long most = static_cast<long long>(a.max_blocks) * a.bs;
+    const long long seen = a.window > 0 ? std::min(most, static_cast<long long>(a.window) + std::min<long long>(a.max_q, kManyRows) + 127)
+                                        : most;
+    a.whole = seen <= kWholeTokens ? 1 : 0;
     int *redo = reinterpret_cast<int *>(a.cuts + grid);
     a.redo = redo;
     a.many_rows = 0;

@@ -21,6 +21,7 @@ struct AttnArgs {
     CutUnit *cuts;
     int N, T, Hq, Hkv, num_blocks, bs, bs_log2, max_blocks, max_q, window, out_bf16;
     float scale_log2;          // scale * log2(e): scores are kept as base-2 exponents
+    int whole;                 // units are not cut (and not joined)
     // requests of more rows than this belong to the many-rows kernel (0: it is not used), but for those it left
     int many_rows;
     const int *redo;           // (N), nullable: requests that the many-rows kernel left

@@ -83,6 +83,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
     if (!INLINE_TOKENS) cudaTriggerProgrammaticLaunchCompletion();   // the token kernel may take its place; it waits below
     const int tid = threadIdx.x, bs = 1 << a.bs_log2;
     const long long cap = static_cast<long long>(a.max_blocks) << a.bs_log2;
+    int count = *a.free_count;
+    if (count < 0 || count > a.num_blocks) {
+        if (tid == 0) atomicOr(err, kErrBadSeqlens);
+        count = 0;
+    }
     if (tid == 0) s_kvmax = 0;
     __syncthreads();
 
@@ -145,28 +150,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
     for (int n = tid; n <= a.N; n += kPlanThreads) a.cu[n] = tok[n];
 
     // ---- finished requests' blocks go on top of the free list, in (request, block) order
-    int count = *a.free_count;
-    if (count < 0 || count > a.num_blocks) {
-        if (tid == 0) atomicOr(err, kErrBadSeqlens);
-        count = 0;
-    }
     const long long rows = static_cast<long long>(ngone) * a.max_blocks;
-    for (long long base = 0; base < rows; base += kPlanThreads) {
-        const long long i = base + tid;
-        int b = -1;
-        if (i < rows) {
-            const int g = static_cast<int>(i / a.max_blocks);
-            int *entry = a.table + static_cast<long long>(gone[g]) * a.max_blocks + (i - static_cast<long long>(g) * a.max_blocks);
-            b = *entry;
-            if (b != -1) *entry = -1;
-            if (b < -1 || b >= a.num_blocks) { atomicOr(err, kErrBadSeqlens); b = -1; }
+    for (long long base = 0; base < rows; base += 4 * kPlanThreads) {      // four entries a thread
+        const long long i0 = base + 4 * tid;
+        int b[4], have = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            b[k] = -1;
+            if (i0 + k < rows) {
+                const int g = static_cast<int>((i0 + k) / a.max_blocks);
+                int *entry = a.table + static_cast<long long>(gone[g]) * a.max_blocks + (i0 + k - static_cast<long long>(g) * a.max_blocks);
+                b[k] = *entry;
+                if (b[k] != -1) *entry = -1;
+                if (b[k] < -1 || b[k] >= a.num_blocks) { atomicOr(err, kErrBadSeqlens); b[k] = -1; }
+            }
+            have += b[k] >= 0 ? 1 : 0;
         }
         int pushed;
-        const int r = block_prefix<int>(b >= 0 ? 1 : 0, &pushed);
-        if (b >= 0) {
-            if (count + r < a.num_blocks) a.free_list[count + r] = b;
-            else atomicOr(err, kErrBadSeqlens);
-        }
+        int at = count + block_prefix<int>(have, &pushed);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (b[k] >= 0) {
+                if (at < a.num_blocks) a.free_list[at] = b[k];
+                else atomicOr(err, kErrBadSeqlens);
+                ++at;
+            }
         count = min(count + pushed, a.num_blocks);
     }
     __syncthreads();

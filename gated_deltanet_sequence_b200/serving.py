@@ -17,7 +17,6 @@ As in :mod:`._lib`, this marshals arguments only.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -29,34 +28,63 @@ from ._lib import _check, _out_opts, _raise, lib
 _BLOCK_SIZES = (16, 32, 64, 128)
 
 
-_HERE = contextlib.nullcontext()
+# The calls below run once a layer and decoded token, on batches whose kernels take a few microseconds, so what they do
+# on the host is kept short: the raw stream handle where torch offers it, one comparison for a tensor that is right.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
 
 
-def _on(dev: torch.device, stream):
-    """(context, raw stream): work for tensors on ``dev``, on ``stream`` or that device's current one. The context
-    makes that device current where it is not (the library launches on the current device)."""
+def _stream_of(dev: torch.device, stream) -> int:
+    """The stream a call for tensors on ``dev`` goes to: ``stream``, or that device's current one."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {dev}")
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _used_on(stream, dev: torch.device, *tensors):
+    """Tensors made here on the current stream and used on ``stream``: kept until that is through with them."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _call(fn: str, dev: torch.device, *args):
+    """One call of the library with ``dev`` current (it launches on the current device)."""
+    f = getattr(lib, fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args)
     else:
-        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    return (_HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)), raw
+        with torch.cuda.device(dev):
+            st = f(*args)
+    if st:
+        _raise(fn, st)
+
+
+def _want(name: str, t: torch.Tensor, shape, dtype, dev):
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return
+    _check(name, t, shape, dtype, dev)
 
 
 def _rows(name: str, t: torch.Tensor, shape, dtype, dev) -> int:
     """Row stride of a (T, heads, d) tensor whose rows are contiguous."""
+    T, h, d = shape
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return h * d
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    _, h, d = shape
     s = t.stride()
     if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
         raise ValueError(f"{name}: heads and columns of a row must be contiguous")
-    if shape[0] <= 1:
+    if T <= 1:
         return h * d
     if s[0] < h * d:
         raise ValueError(f"{name}: rows overlap (row stride {s[0]} < {h * d})")
@@ -117,39 +145,29 @@ def gdn_plan_batch(ctx_lens, new_lens, block_table, free_list, free_count, block
     """Block tables, slot maps and packed offsets of a step from the requests' lengths (N,) int32: ctx_lens tokens
     cached, new_lens tokens brought (0: waiting, -1: finished, its blocks are freed). Updates block_table
     (N, max_blocks), free_list (num_blocks,) and free_count (1,) in place, fills ``plan`` and returns it."""
-    dev = plan.device
-    N = plan.N
-    _check("ctx_lens", ctx_lens, (N,), torch.int32, dev)
-    _check("new_lens", new_lens, (N,), torch.int32, dev)
+    dev, N = plan.device, plan.N
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected (N, max_blocks), got {tuple(block_table.shape)}")
     mb, nb = block_table.shape[1], free_list.numel()
-    _check("block_table", block_table, (N, mb), torch.int32, dev)
-    _check("free_list", free_list, (nb,), torch.int32, dev)
-    _check("free_count", free_count, (1,), torch.int32, dev)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        st = lib.gdn_plan_batch(ctx_lens.data_ptr(), new_lens.data_ptr(), N, block_table.data_ptr(), mb,
-                                free_list.data_ptr(), free_count.data_ptr(), nb, int(block_size), plan.T, *plan._args, raw)
-    _raise("gdn_plan_batch", st)
+    for name, t, shape in (("ctx_lens", ctx_lens, (N,)), ("new_lens", new_lens, (N,)), ("block_table", block_table, (N, mb)),
+                           ("free_list", free_list, (nb,)), ("free_count", free_count, (1,))):
+        _want(name, t, shape, _i32, dev)
+    _call("gdn_plan_batch", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), N, block_table.data_ptr(), mb,
+          free_list.data_ptr(), free_count.data_ptr(), nb, block_size, plan.T, *plan._args, _stream_of(dev, stream))
     return plan
 
 
 def gdn_kv_append(cache: KvCache, k, v, slot_map, stream=None) -> KvCache:
     """Write k, v (T, Hkv, d) bf16 / fp32 into the cache rows slot_map (T,) int32 names (-1: skipped). The rows of one
     block must be consecutive, as BatchPlan.slot_map has them."""
-    T = k.shape[0]
-    shape = torch.Size((T, cache.heads, cache.d))
-    ks = _rows("k", k, shape, k.dtype, cache.device)
-    vs = _rows("v", v, shape, k.dtype, cache.device)
-    _check("slot_map", slot_map, (T,), torch.int32, cache.device)
-    dt = _lib._dtype_code(k)
-    ctx, raw = _on(cache.device, stream)
+    dev, T = cache.device, k.shape[0]
+    shape = (T, cache.heads, cache.d)
+    ks = _rows("k", k, shape, k.dtype, dev)
+    vs = _rows("v", v, shape, k.dtype, dev)
+    _want("slot_map", slot_map, (T,), _i32, dev)
     kc, vc, kscale, vscale = cache._args
-    with ctx:
-        st = lib.gdn_kv_append(k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), kc, vc, kscale, vscale, T,
-                               cache.heads, cache.d, cache.num_blocks, cache.block_size, dt, raw)
-    _raise("gdn_kv_append", st)
+    _call("gdn_kv_append", dev, k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), kc, vc, kscale, vscale, T,
+          cache.heads, cache.d, cache.num_blocks, cache.block_size, _lib._dtype_code(k), _stream_of(dev, stream))
     return cache
 
 
@@ -177,40 +195,40 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
         raise ValueError(f"q: {Hq} query heads over {cache.heads} KV heads")
     qs = _rows("q", q, q.shape, q.dtype, dev)
     N = kv_lens.numel()
-    _check("kv_lens", kv_lens, (N,), torch.int32, dev)
-    _check("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected (N, max_blocks), got {tuple(block_table.shape)}")
     mb = block_table.shape[1]
-    _check("block_table", block_table, (N, mb), torch.int32, dev)
-    odt = o.dtype if o is not None else (out_dtype or torch.float32)
-    if odt not in (torch.float32, torch.bfloat16):
+    _want("kv_lens", kv_lens, (N,), _i32, dev)
+    _want("cu_seqlens", cu_seqlens, (N + 1,), _i32, dev)
+    _want("block_table", block_table, (N, mb), _i32, dev)
+    odt = o.dtype if o is not None else (out_dtype or _f32)
+    if odt is not _f32 and odt is not _bf16:
         raise TypeError(f"o / out_dtype must be float32 or bfloat16, got {odt}")
     dt = _lib._dtype_code(q)
-    ctx, raw = _on(dev, stream)
-    need = lib.gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, int(max_q_len))
-    with ctx:
-        if o is None:
-            o = torch.empty(T, Hq, d, dtype=odt, device=dev)
-        else:
-            _check("o", o, (T, Hq, d), odt, dev)
-        if lse is True:
-            lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
-        elif lse is not None:
-            _check("lse", lse, (T, Hq), torch.float32, dev)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-            if stream is not None and isinstance(stream, torch.cuda.Stream):
-                workspace.record_stream(stream)     # it may be freed before that stream is through with it
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        kc, vc, kscale, vscale = cache._args
-        st = lib.gdn_kv_attn(q.data_ptr(), qs, kc, vc, kscale, vscale, block_table.data_ptr(), cu_seqlens.data_ptr(),
-                             kv_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), N, T, Hq, cache.heads,
-                             d, cache.num_blocks, cache.block_size, mb, int(max_q_len), int(window), float(scale),
-                             dt, _lib.GDN_BF16 if odt == torch.bfloat16 else _lib.GDN_F32, raw)
-    _raise("gdn_kv_attn", st)
+    raw = _stream_of(dev, stream)
+    need = lib.gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, max_q_len)
+    new = []
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=odt, device=dev)
+        new.append(o)
+    else:
+        _want("o", o, (T, Hq, d), odt, dev)
+    if lse is True:
+        lse = torch.empty((T, Hq), dtype=_f32, device=dev)
+        new.append(lse)
+    elif lse is not None:
+        _want("lse", lse, (T, Hq), _f32, dev)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        new.append(workspace)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _used_on(stream, dev, *new)
+    kc, vc, kscale, vscale = cache._args
+    _call("gdn_kv_attn", dev, q.data_ptr(), qs, kc, vc, kscale, vscale, block_table.data_ptr(), cu_seqlens.data_ptr(),
+          kv_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), N, T, Hq, cache.heads, d, cache.num_blocks, cache.block_size, mb,
+          max_q_len, window, scale, dt, _lib.GDN_BF16 if odt is _bf16 else _lib.GDN_F32, raw)
     return o, lse
 
 
@@ -231,30 +249,29 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
     vs = _rows("v", v, torch.Size((T, Hv, dv)), q.dtype, dev)
     if Hk == 0 or Hv % Hk != 0:
         raise ValueError(f"{Hv} value heads over {Hk} key heads")
-    _check("beta", beta, (T, Hv), torch.float32, dev, required=False)
+    if beta is not None:
+        _want("beta", beta, (T, Hv), _f32, dev)
     vec = _lib._check_gate(g, (T, Hv), dk, dev)
     if state.dim() != 4:
         raise ValueError(f"state: expected (n_slots, Hv, dk, dv), got {tuple(state.shape)}")
-    _check("state", state, (state.shape[0], Hv, dk, dv), torch.float32, dev)
+    _want("state", state, (state.shape[0], Hv, dk, dv), _f32, dev)
     N = slots.numel()
-    _check("slots", slots, (N,), torch.int32, dev)
+    _want("slots", slots, (N,), _i32, dev)
     if cu_seqlens is None:
         if T != N:
             raise ValueError(f"{T} rows for {N} slots: give cu_seqlens")
     else:
-        _check("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+        _want("cu_seqlens", cu_seqlens, (N + 1,), _i32, dev)
     odt, opts = _out_opts(o, out_dtype, d_skip, Hv, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     dt = _lib._dtype_code(q)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if o is None:
-            o = torch.empty(T, Hv, dv, dtype=odt, device=dev)
-        else:
-            _check("o", o, (T, Hv, dv), odt, dev)
-        st = lib.gdn_decode_slots(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
-                                  None if beta is None else beta.data_ptr(), None if g is None else g.data_ptr(),
-                                  state.data_ptr(), slots.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                                  o.data_ptr(), N, T, Hk, Hv, state.shape[0], dk, dv, float(scale), dt,
-                                  None if opts is None else ctypes.byref(opts), raw)
-    _raise("gdn_decode_slots", st)
+    raw = _stream_of(dev, stream)
+    if o is None:
+        o = torch.empty((T, Hv, dv), dtype=odt, device=dev)
+        _used_on(stream, dev, o)
+    else:
+        _want("o", o, (T, Hv, dv), odt, dev)
+    _call("gdn_decode_slots", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+          None if beta is None else beta.data_ptr(), None if g is None else g.data_ptr(), state.data_ptr(),
+          slots.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(), N, T, Hk, Hv,
+          state.shape[0], dk, dv, scale, dt, None if opts is None else ctypes.byref(opts), raw)
     return o
