@@ -120,11 +120,6 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = pack_h2(x - f.x, y - f.y);
 }
-__device__ __forceinline__ uint32_t nan_halves(uint32_t h) {      // 0xffff in the halves that are NaN
-    const __half2 x = *reinterpret_cast<const __half2 *>(&h);
-    return __hneu2_mask(x, x);
-}
-
 // How queries enter Q K^T. kF8: as two e4m3 parts (bf16 queries with a bf16 output: the codes of K are then an
 // operand as they are); kF16, kF16x2: as one or two fp16 parts, K's codes converted.
 enum QKind { kF8, kF16, kF16x2 };
@@ -140,6 +135,7 @@ struct Worker {
     float m[2], l[2], rf[2];       // rows g and g + 8: reference of the exponents, this lane's part of the sum, score factor
     int hi[2], lo[2];              // positions a row sees: lo .. hi
     float vu;                      // V scale that the accumulators are in units of (0: none yet)
+    bool saw_nan;                  // a NaN of V was taken out of an edge step
 
     __device__ __forceinline__ static int token_of(int n) { return D == 128 ? (n & 1) * 4 + (n >> 1) : n; }
 
@@ -210,11 +206,10 @@ struct Worker {
         }
     }
 
-    // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's two
-    // halves; EDGE: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
-    template <bool EDGE>
+    // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's halves;
+    // edge: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
     __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[HV], const float (&vs)[HV],
-                                         uint32_t tok) {
+                                         uint32_t tok, bool edge) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
         // (the four token groups side by side: a group's own products are a chain)
         float x[4][4];
@@ -273,14 +268,20 @@ struct Worker {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[j][i] = fmaf(x[j][i], rk[HV == 1 ? 0 : j >> 1][i >> 1], -base[i >> 1]);
-                    if (EDGE) x[j][i] = sees(j, i) ? x[j][i] : kNegInf;
-                    top = fmaxf(top, x[j][i]);
-                }
+                for (int i = 0; i < 4; ++i) x[j][i] = fmaf(x[j][i], rk[HV == 1 ? 0 : j >> 1][i >> 1], -base[i >> 1]);
         }
-        if (__any_sync(0xffffffffu, top > kSlack || none[0] || none[1])) {
-            float f[2];
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[j][i] = sees(j, i) ? x[j][i] : kNegInf;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
+        // the accumulators' factors: of the references, and of V's unit
+        float f[2] = {1.f, 1.f};
+        const bool move = __any_sync(0xffffffffu, top > kSlack || none[0] || none[1]);
+        if (move) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float mx = kNegInf;
@@ -288,7 +289,6 @@ struct Worker {
                 for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[j][2 * r], x[j][2 * r + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                f[r] = 1.f;
                 if (mx > (none[r] ? kNegInf : 0.f)) {
                     f[r] = none[r] ? 0.f : ex2(-mx);
                     m[r] = none[r] ? mx : m[r] + mx;
@@ -297,7 +297,11 @@ struct Worker {
                 }
                 l[r] *= f[r];
             }
-            scale_o(f[0], f[1]);
+        }
+        if (move || vs[0] != vu) {
+            const float u = vu == 0.f ? 1.f : vu / vs[0];
+            scale_o(f[0] * u, f[1] * u);
+            vu = vs[0];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -308,10 +312,11 @@ struct Worker {
             }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
-            if (hf < HV && vs[hf < HV ? hf : 0] != vu) {
-                const float u = vu == 0.f ? 1.f : vu / vs[hf < HV ? hf : 0];
-                scale_o(u, u);
-                vu = vs[hf < HV ? hf : 0];
+            if constexpr (HV == 2) {
+                if (hf == 1 && vs[1] != vu) {
+                    scale_o(vu / vs[1], vu / vs[1]);
+                    vu = vs[1];
+                }
             }
             uint32_t p[4], pl[4];
             float(&xa)[4] = x[2 * hf], (&xb)[4] = x[2 * hf + 1];
@@ -342,28 +347,20 @@ struct Worker {
                                  : "r"(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
                 }
             }
-            uint32_t keep[2] = {0xffffffffu, 0xffffffffu}, seen[4] = {};
-            bool nans = false;
-            if constexpr (EDGE) {
-                // Rows that do not exist hold anything: their values are taken out. A NaN among values that some row
-                // does not see must reach the rows that do, and 0 * NaN must not reach the others: where there is one,
-                // its rows are those with a 1 (token seen) against a 1 (a NaN there).
-                keep[0] = (((tok >> ra) & 1u) ? 0xffffu : 0u) | (((tok >> rb) & 1u) ? 0xffff0000u : 0u);
-                keep[1] = (((tok >> (ra + 8)) & 1u) ? 0xffffu : 0u) | (((tok >> (rb + 8)) & 1u) ? 0xffff0000u : 0u);
-                bool any = false;
+            if (edge) {
+                // Rows that do not exist hold anything, and 0 * NaN would reach rows that do not see the NaN: both are taken
+                // out, and a NaN is noted (the rows it belongs to are found when the unit is done).
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (i & 1 ? rb : ra) + (i >> 1) * 8;
+                    const uint32_t keep = (tok >> r) & 1u ? 0xffffffffu : 0u;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        const uint32_t z = (v[i][w] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;      // a zero byte is a NaN code
-                        any |= ((z - 0x01010101u) & ~z & 0x80808080u) != 0u;
+                        const uint32_t isnan = __vcmpeq4(v[i][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) & keep;
+                        saw_nan |= isnan != 0u;
+                        v[i][w] &= keep & ~isnan;
                     }
-                nans = __any_sync(0xffffffffu, any);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (sees(2 * hf + (r >> 1), 2 * (r & 1) + e)) seen[r] |= 0x3c00u << (16 * e);
+                }
             }
 #pragma unroll
             for (int w = 0; w < W; ++w)
@@ -371,22 +368,9 @@ struct Worker {
                 for (int q = 0; q < 4; ++q) {
                     // column 4 w + q of the lane's chunk: the two rows' bytes side by side, then as fp16 pair
                     const uint32_t sel = q | ((4 + q) << 4);
-                    uint32_t b0 = e4m3x2_to_h2(__byte_perm(v[0][w], v[1][w], sel));
-                    uint32_t b1 = e4m3x2_to_h2(__byte_perm(v[2][w], v[3][w], sel));
+                    const uint32_t b0 = e4m3x2_to_h2(__byte_perm(v[0][w], v[1][w], sel));
+                    const uint32_t b1 = e4m3x2_to_h2(__byte_perm(v[2][w], v[3][w], sel));
                     float(&acc)[4] = o[4 * w + q];
-                    if constexpr (EDGE) {
-                        b0 &= keep[0];
-                        b1 &= keep[1];
-                        if (nans) {
-                            const uint32_t n0 = nan_halves(b0), n1 = nan_halves(b1);
-                            b0 &= ~n0;
-                            b1 &= ~n1;
-                            float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(hit, seen, n0 & 0x3c003c00u, n1 & 0x3c003c00u);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) acc[r] = hit[r] > 0.f ? __int_as_float(0x7fffffff) : acc[r];
-                        }
-                    }
                     if constexpr (PSPLIT) {
                         // an fp32 output: the tensor core's own running sum truncates, so each half's sum starts anew
                         // and is added in fp32
@@ -548,6 +532,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
         for (int i = 0; i < W::NT; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
         w.vu = 0.f;
+        w.saw_nan = false;
 
         const int lo_last = a.window > 0 ? p_last - a.window + 1 : 0;
         bool ok = true;
@@ -598,22 +583,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             st = st + 1 == S::kStages ? 0 : st + 1;
             return sk;
         };
-        // Runs of steps of one kind, each in a loop of its own: with both kinds in one loop the accumulators changed
-        // registers at every turn (300 moves a step).
-        int i = 0;
-        Step nx;
-        if (nstep > 0) nx = look(0);
-        while (i < nstep) {
-            while (i < nstep && !nx.edge) {
-                const uint32_t sk = turn(i);
-                if (ok) w.template step<false>(sk, sk + S::kStepBytes, nx.t, nx.ks, nx.vs, nx.tok);
-                if (++i < nstep) nx = look(i);
-            }
-            while (i < nstep && nx.edge) {
-                const uint32_t sk = turn(i);
-                if (ok && nx.tok != 0u) w.template step<true>(sk, sk + S::kStepBytes, nx.t, nx.ks, nx.vs, nx.tok);
-                if (++i < nstep) nx = look(i);
-            }
+        for (int i = 0; i < nstep; ++i) {
+            const Step x = look(i);
+            const uint32_t sk = turn(i);
+            if (ok && x.tok != 0u) w.step(sk, sk + S::kStepBytes, x.t, x.ks, x.vs, x.tok, x.edge);
         }
 
         // ---- the four warps' parts of each row
@@ -626,7 +599,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 s_ml[warp][g + 8 * r][1] = w.l[r];
             }
         }
-        __syncthreads();                    // every warp is through its ring
+        const bool nans = __syncthreads_or(w.saw_nan);      // (and every warp is through its ring)
         float *mg = reinterpret_cast<float *>(smem);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -670,6 +643,18 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 acc[3] = fmaf(v.w, f, acc[3]);
             }
             const int R = rt * kRows + r;
+            if (nans) {        // rare: the row's own positions are looked through for NaN in these columns
+                const int pos = rw.kv - rw.qlen + R / G, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                for (int t = max(t_lo, lo); t < min(t_hi, pos + 1); ++t) {
+                    const int id = table[t >> a.bs_log2];
+                    if (id < 0 || id >= a.num_blocks) continue;
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                        a.v_codes + ((((static_cast<long long>(id) * a.Hkv + h) << a.bs_log2) + (t & (a.bs - 1))) * D + x));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (((v >> (8 * k)) & 0x7fu) == 0x7fu) acc[k] = __int_as_float(0x7fffffff);
+                }
+            }
             if (whole) {
                 store_row<4>(a, rw.row0 + R / G, h * G + R % G, D, x, acc, ll, mm);
             } else {
@@ -801,10 +786,11 @@ size_t kv_attn_ws_bytes(int N, int d) {
 gdn_status_t launch_kv_prompt(const void *kc, const void *vc, const AttnArgs &a, int d, int *redo, cudaStream_t stream);
 
 constexpr int kManyRows = 64;
-constexpr int kWholeTokens = 1024;
+constexpr int kWholeTokens = 256, kWholeTokensMany = 1024;
 
 gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, bool in_f32, bool out_f32,
                             cudaStream_t stream) {
+    a.v_codes = static_cast<const uint8_t *>(vc);
     a.err = device_error_word();
     if (!a.err) return GDN_ERR_CUDA;
     a.wait_limit = wait_limit_cycles();
@@ -814,11 +800,13 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
         return GDN_ERR_CUDA;
     const int grid = kv_attn_grid(d);
     a.cuts = reinterpret_cast<CutUnit *>(a.ws + grid * 2 * part_floats(d));
-    // Contexts (or windows) that the table bounds to this many tokens are not cut
+    // Contexts (or windows) that the table bounds to kWholeTokens are not cut, nor those up to kWholeTokensMany where there
+    // are units for half the blocks: no join, and fewer units begun (8 KV heads, d = 128, cut / not cut: one request of
+    // 100 tokens 10.5 / 8.7 us, 32 of 700 23.9 / 18.7 us, but one of 700 10.7 / 15.5 us)
     const long long most = static_cast<long long>(a.max_blocks) * a.bs;
     const long long seen = a.window > 0 ? std::min(most, static_cast<long long>(a.window) + std::min<long long>(a.max_q, kManyRows) + 127)
                                         : most;
-    a.whole = seen <= kWholeTokens ? 1 : 0;
+    a.whole = seen <= kWholeTokens || (seen <= kWholeTokensMany && 2ll * a.N * a.Hkv >= grid) ? 1 : 0;
     int *redo = reinterpret_cast<int *>(a.cuts + grid);
     a.redo = redo;
     a.many_rows = 0;

@@ -15,6 +15,7 @@ struct AttnArgs {
     const void *q;
     long long q_stride;
     const float *k_scale, *v_scale;
+    const uint8_t *v_codes;
     const int *table, *cu, *kv_lens;
     void *o;
     float *lse, *ws;

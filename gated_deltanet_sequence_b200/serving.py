@@ -18,6 +18,7 @@ As in :mod:`._lib`, this marshals arguments only.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -171,6 +172,7 @@ def gdn_kv_append(cache: KvCache, k, v, slot_map, stream=None) -> KvCache:
     return cache
 
 
+@functools.lru_cache(maxsize=1024)
 def gdn_kv_attn_workspace_bytes(N: int, T: int, Hq: int, Hkv: int, d: int, max_q_len: int = 1) -> int:
     """Bytes of device workspace gdn_kv_attn needs (0 for unsupported sizes)."""
     return int(lib.gdn_kv_attn_workspace_bytes(N, T, Hq, Hkv, d, max_q_len))
@@ -206,20 +208,20 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
         raise TypeError(f"o / out_dtype must be float32 or bfloat16, got {odt}")
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
-    need = lib.gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, max_q_len)
+    need = gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, max_q_len)
     new = []
     if o is None:
-        o = torch.empty((T, Hq, d), dtype=odt, device=dev)
+        o = q.new_empty((T, Hq, d), dtype=odt)
         new.append(o)
     else:
         _want("o", o, (T, Hq, d), odt, dev)
     if lse is True:
-        lse = torch.empty((T, Hq), dtype=_f32, device=dev)
+        lse = q.new_empty((T, Hq), dtype=_f32)
         new.append(lse)
     elif lse is not None:
         _want("lse", lse, (T, Hq), _f32, dev)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
         new.append(workspace)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -266,7 +268,7 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
     if o is None:
-        o = torch.empty((T, Hv, dv), dtype=odt, device=dev)
+        o = q.new_empty((T, Hv, dv), dtype=odt)
         _used_on(stream, dev, o)
     else:
         _want("o", o, (T, Hv, dv), odt, dev)
