@@ -38,7 +38,7 @@ __host__ __device__ constexpr long long part_floats(int d) { return 32 + 16ll * 
 
 // What a unit costs beside its tiles (its queries, the warps' merge, its rows), in tiles. Without it the shares of
 // short contexts took longest.
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 3;
 
 // A request's part of the work line: (Hkv x row_tiles) units of kUnitCost + `tiles` places, a place for each kv tile
 // (128 tokens) from tile0 on. A request with rows has one tile at least, so that every unit's rows are written.
