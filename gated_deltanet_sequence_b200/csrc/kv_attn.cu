@@ -70,25 +70,6 @@ __device__ __forceinline__ void e4m3_to_h2(uint32_t w, uint32_t &lo, uint32_t &h
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
-// Wait for phase `parity`, at most about `limit` cycles. The first look does not suspend the thread, so that a
-// limit shorter than the hardware's own suspension is kept too.
-__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, long long limit) {
-    const uint32_t b = smem_u32(bar);
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(b), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    const long long t0 = clock64();
-    do {
-        if (clock64() - t0 > limit) return false;
-    } while (!mbar_try_wait(b, parity));
-    return true;
-}
 // the same for an e4m3 query: D += A (16 x 32, e4m3) B (32 x 8, e4m3)
 __device__ __forceinline__ void mma16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -569,11 +550,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             if (ok && (live & (1u << st))) {
                 const uint32_t par = (phase >> st) & 1u;
-                if (!ring_wait(&s_bar[warp][st], par, a.wait_limit)) {
+                if (!bounded_wait(&s_bar[warp][st], par, a.wait_limit)) {
                     // gave up: reported, and the copy still in flight is waited for (with the drain's limit)
                     // before its buffer is used again
                     if (lane == 0) atomicOr(a.err, kErrWaitTimeout);
-                    ok = ring_wait(&s_bar[warp][st], par, kDrainLimitCycles);
+                    ok = bounded_wait(&s_bar[warp][st], par, kDrainLimitCycles);
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 phase ^= 1u << st;

@@ -121,6 +121,30 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, int blk, int nbloc
     __syncthreads();
 }
 
+// Whether phase `parity` is complete, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for phase `parity`, at most about `limit` cycles. The first look does not suspend the thread, so that a
+// limit shorter than the hardware's own suspension is kept too.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, long long limit) {
+    const uint32_t b = ptx::smem_u32(bar);
+    if (mbar_test_wait(b, parity)) return true;
+    const long long t0 = clock64();
+    do {
+        if (clock64() - t0 > limit) return false;
+    } while (!ptx::mbar_try_wait(b, parity));
+    return true;
+}
+
 // 4 values of a row as fp32 (zeros for a null pointer)
 __device__ __forceinline__ void load4(const float *p, float *f) {
     const float4 x = p ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);

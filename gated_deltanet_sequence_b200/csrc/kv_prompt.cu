@@ -39,6 +39,7 @@ constexpr float kMaxSum = 16384.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMinScale = 7.888609052210118e-31f;      // 2^-100: a block of zeros
 constexpr float kSpread = 4096.f;
+constexpr float kMinNormal = 1.1754943508222875e-38f;    // 2^-126
 
 enum : int {
     B_Q = 0,          // 8 warps: queries written
@@ -194,6 +195,7 @@ __device__ __forceinline__ Rows unit_rows(const AttnArgs &a, int n) {
 }
 // first row tile of the request that ends in kv tile e or later (rows.tiles: none)
 __device__ __forceinline__ int first_from(const Rows &q, int e, int G) {
+    if (e <= 0) return 0;                // (rows before position 0 count as tile 0's)
     const long long need = static_cast<long long>(G) * (static_cast<long long>(e) * kTok - q.p0);     // last row >= need
     if (need <= 0) return 0;
     const long long t = (need + kUnitRows) / kUnitRows - 1;
@@ -214,7 +216,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int idx, Unit *out)
         }
         return __reduce_add_sync(0xffffffffu, c);
     };
-    // the largest e with more than idx tiles from it on (rows before position 0 end "in" tile 0)
+    // the largest e with more than idx tiles from it on
     int lo = 0, hi = a.max_blocks * a.bs / kTok + 1;
     if (from(0) <= idx) return false;
     while (hi - lo > 1) {
@@ -303,9 +305,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
     // a warp's wait: most phases are complete when they are looked at, and the abort flag is looked at only in the others
     auto wait = [&](int b, uint32_t parity) {
-        const bool now = mbar_try_wait(smem_u32(&bars[b]), parity);
+        const bool now = mbar_test_wait(smem_u32(&bars[b]), parity);
         if (__all_sync(0xffffffffu, now)) return true;
-        return __all_sync(0xffffffffu, ctl.wait(b, parity)) != 0;
+        const bool ok = now || (!ctl.aborted() && (bounded_wait(&bars[b], parity, ctl.limit) || ctl.give_up()));
+        return __all_sync(0xffffffffu, ok) != 0;
     };
     // The groups keep a row's 128 scores in registers: 256 threads take 192 each, the other 256 64 (65536 in all, what
     // the block was launched with)
@@ -576,7 +579,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const int c_hi = hi - t0, c_lo = lo - t0;    // columns this row sees
             float k[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) k[q] = rf * s_ks[slot * 8 + 4 * hf + q];
+            for (int q = 0; q < 4; ++q) k[q] = fmaxf(rf * s_ks[slot * 8 + 4 * hf + q], kMinNormal);   // never 0: -inf stays -inf
             // Weights against the row's reference m. m is the largest exponent of the row's first half tile with something
             // to see, and stays while a half tile's weights sum to at most kMaxSum (then none of them is beyond
             // fp16): the sum is there anyway, so most half tiles need no maximum, and their accumulators no rescaling.
@@ -629,7 +632,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         for (int w = 4; w >= 1; w >>= 1)
 #pragma unroll
                             for (int c = 0; c < w; ++c) x[c] = fmaxf(x[c], x[c + w]);
-                        if (x[0] > kNegInf) top = fmaxf(top, x[0] * (rf * s_ks[slot * 8 + 4 * hf + 2 * ch + q]));
+                        if (x[0] > kNegInf) top = fmaxf(top, x[0] * fmaxf(rf * s_ks[slot * 8 + 4 * hf + 2 * ch + q], kMinNormal));
                     }
                 }
                 if (top > m) {

@@ -6,7 +6,10 @@ gdn_decode_slots against fp64; the sizes, masks and inputs where each can go wro
 Tolerances of gdn_kv_attn, for a row with weights w_p = exp(s_p - max s), A = sum w |v| / sum w:
   scores     each is a sum of d products in fp32 (tensor-core accumulation truncates: 2^-23 of the running sum of
              magnitudes a step), with fp32 queries cut to 22 bits: ds <= scale * sum |q k| * (d + 4) * 2^-23. A weight
-             moves by e^ds, numerator and denominator alike: 2 ds A (ds < 0.1).
+             moves by e^ds, numerator and denominator alike: 2 ds A (ds < 0.1). With bf16 queries and a bf16 output the
+             queries are two e4m3 parts, scaled so that the row's largest is above 224: exact, but for a half step
+             of the smallest part, 2^-10, so at most 2^-10 / 224 of the row's largest: ds grows by
+             scale * 2^-10 / 224 * max |q| * sum |k|.
   weights    ex2 and the scale product: 2^-21 A; as one fp16 part 2^-11 A, and below 2^-14 an absolute 2^-25 each
              (n 2^-25 max|v|); as two parts 2^-22 A.
   sums       of n terms in fp32, at most n 2^-24 each way but at most 2^-11 A for the sizes here.
@@ -317,7 +320,7 @@ def test_append_reports_slots_out_of_range(S, lib):
 
 
 # ---------------------------------------------------------------- attention
-def attn_ref(cache, q, table, cu, kv, window, scale):
+def attn_ref(cache, q, table, cu, kv, window, scale, parts=False):
     """fp64 on the CPU: o, lse, and the tolerance's pieces A = sum w|v| / sum w, ds and max|v| of each row."""
     q = q.double().cpu()
     k, v = ((c.cpu().float().double() * s.cpu().double()[:, :, None, None]) for c, s in
@@ -344,6 +347,8 @@ def attn_ref(cache, q, table, cu, kv, window, scale):
                 w = torch.exp(s - r)
                 lse[t, h], o[t, h], A[t, h] = r, w @ vs, w @ vs.abs()
                 ds[t, h] = abs(scale) * (ks.abs() @ qq.abs()).max() * (d + 4) * 2.0 ** -23
+                if parts:
+                    ds[t, h] += abs(scale) * 2.0 ** -10 / 224 * qq.abs().max() * ks.abs().sum(-1).max()
                 vm[t, h] = vs.abs().max()
     return o, lse, A, ds, vm
 
@@ -374,7 +379,7 @@ def attn_check(S, lib, cache, q, table, tab, cu, kv, window, scale, out, max_q=N
     S.gdn_kv_attn(cache, qq, tab, i32(cu), i32(kv), max_q_len=mq, window=window, scale=scale, o=o, lse=lse)
     assert lib.gdn_sync_status() == 0
     assert (o[T:] == 7).all() and (lse[T:] == 7).all()
-    ro, rl, A, ds, vm = attn_ref(cache, q, table, cu, kv, window, scale)
+    ro, rl, A, ds, vm = attn_ref(cache, q, table, cu, kv, window, scale, q.dtype == out == torch.bfloat16)
     o, lse = o[:T].double().cpu(), lse[:T].double().cpu()
     n = max([1] + list(kv))
     sums = min(n * 2.0 ** -23, 2.0 ** -11)
@@ -548,6 +553,108 @@ def test_attn_gives_up_on_a_wait_and_reports_it(S, lib):
         lib.gdn_set_wait_limit_for_testing(0)
     o, _ = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), scale=0.1)
     assert lib.gdn_sync_status() == 0 and torch.equal(o, ref)
+
+
+PROMPT = {  # kv lengths, query rows: requests of more than 64 rows (tokens x heads of a KV head) take the many-rows kernel
+    "just over": ([65], [65]),
+    "one tile": ([128], [128]),
+    "ragged": ([300, 5, 131, 257], [300, 1, 67, 129]),
+    "over a context": ([700, 600], [200, 33]),
+    "more rows than tokens": ([100, 0, 20], [130, 80, 1]),
+    "long": ([1500], [310]),
+}
+
+
+@pytest.mark.parametrize("case", list(PROMPT))
+@pytest.mark.parametrize("Hkv,G,d,bs,window,scale", [
+    (1, 1, 128, 64, 0, 0.09), (2, 4, 128, 16, 0, 0.09), (1, 3, 64, 32, 0, 0.125), (2, 1, 64, 128, 100, 0.125),
+    (1, 2, 128, 128, 1, -0.09), (1, 8, 64, 16, 300, 0.125), (1, 1, 128, 32, 64, 0.0),
+])
+def test_attn_prompts_match_fp64(S, lib, case, Hkv, G, d, bs, window, scale):
+    kv, ql = PROMPT[case]
+    args = attn_case(S, kv, ql, Hkv, G, d, bs, torch.bfloat16, seed=len(case) + d + bs, fill=0x7f)
+    attn_check(S, lib, *args, kv, window, scale, torch.bfloat16)
+
+
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 64)])
+def test_attn_prompt_scales_far_apart(S, lib, d, bs):
+    """V scales of neighbouring blocks 2^40 apart (fp16 cannot hold them together), blocks of zeros, queries of 1e-20."""
+    kv, ql = [300, 90], [150, 80]
+    cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, d, bs, torch.bfloat16, seed=31)
+    zero = table[0][1]
+    for c, sc in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        c.view(torch.uint8)[zero] = 0
+        sc[zero] = 2.0 ** -100
+    attn_check(S, lib, cache, (q.float() * 1e-20).bfloat16(), table, tab, cu, kv, 0, 1e19, torch.bfloat16)
+    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.1, torch.bfloat16)
+    cache.v_scale.copy_(torch.exp2(torch.randint(-30, 10, cache.v_scale.shape, generator=_gen(1), device=DEV).float()))
+    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("window", [0, 50])
+def test_attn_prompt_nan_reaches_the_rows_that_see_it(S, lib, where, window):
+    kv, ql, Hkv, G, d, bs = [200, 150], [120, 150], 2, 1, 64, 16
+    cache, q, table, tab, cu = attn_case(S, kv, ql, Hkv, G, d, bs, torch.bfloat16, seed=78)
+    at = 133
+    hole = cache.k if where == "k" else cache.v
+    hole.view(torch.uint8)[table[0][at // bs], 1, at % bs, 9] = 0xff
+    o, _ = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), max_q_len=150, window=window, scale=0.125, out_dtype=torch.bfloat16)
+    assert lib.gdn_sync_status() == 0
+    bad = torch.isnan(o).cpu()
+    for i in range(ql[0]):
+        pos = kv[0] - ql[0] + i
+        hit = pos >= at and (window == 0 or pos - window < at)
+        assert not bad[i, 0].any() and bool(bad[i, 1, 9]) == hit and bool(bad[i, 1].any()) == hit, i
+        if where == "v":
+            assert int(bad[i, 1].sum()) == int(hit)
+    assert not bad[cu[1]:].any()
+
+
+def test_attn_prompt_bad_pages_graphs_and_waits(S, lib):
+    kv, ql = [400, 30, 300], [400, 1, 90]
+    cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, 128, 64, torch.bfloat16, seed=14)
+    cu_t, kv_t = i32(cu), i32(kv)
+    kw = dict(max_q_len=400, scale=0.09, out_dtype=torch.bfloat16)
+    good, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
+    assert lib.gdn_sync_status() == 0
+    for b in (-1, cache.num_blocks, 2 ** 31 - 1):             # a page that does not exist: its positions are left out
+        t2 = tab.clone()
+        t2[0, 2] = b
+        o, _ = S.gdn_kv_attn(cache, q, t2, cu_t, kv_t, **kw)
+        assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG and lib.gdn_sync_status() == 0
+        assert torch.equal(o[:128], good[:128]) and torch.equal(o[400:], good[400:]) and torch.isfinite(o).all()
+        assert not torch.equal(o[128:400], good[128:400])
+    # a request with more rows than max_q_len says is left out, by both kernels
+    o = torch.full_like(good, 7.0)
+    S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, max_q_len=100, scale=0.09, o=o)
+    assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG
+    assert (o[:400] == 7).all() and torch.equal(o[400:], good[400:])
+    # captured and replayed with other lengths; two streams at once
+    o = torch.zeros_like(good)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, o=o, **{k: v for k, v in kw.items() if k != "out_dtype"})
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, stream=st, **kw)[0] for st in side for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, good) for x in outs)
+    kv_t.copy_(i32([390, 30, 299]))
+    graph.replay()
+    torch.cuda.synchronize()
+    want, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
+    assert torch.equal(o, want) and not torch.equal(o, good) and lib.gdn_sync_status() == 0
+    lib.gdn_set_wait_limit_for_testing(1)
+    try:
+        S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
+        assert lib.gdn_sync_status() == lib.GDN_ERR_TIMEOUT
+        while lib.gdn_sync_status() != 0:
+            pass
+    finally:
+        lib.gdn_set_wait_limit_for_testing(0)
+    o, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
+    assert torch.equal(o, want) and lib.gdn_sync_status() == 0
 
 
 # ---------------------------------------------------------------- recurrence over slots
