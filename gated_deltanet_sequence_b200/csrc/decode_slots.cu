@@ -57,6 +57,8 @@ decode_slots_kernel(const IT *__restrict__ q, const IT *__restrict__ k, const IT
     if (t0 == t1) return;
 
     float *S = a.state + (static_cast<long long>(slot) * a.Hv + h) * (DK * DV);
+    if (!in_bounds((static_cast<long long>(slot) * a.Hv + h + 1) * (DK * DV) - 1, static_cast<long long>(a.n_slots) * a.Hv * DK * DV, err))
+        return;
     float4 st[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) st[i] = ld_global4(S + (rg + RG * i) * DV + 4 * cg);
@@ -165,13 +167,14 @@ decode_slots_kernel(const IT *__restrict__ q, const IT *__restrict__ k, const IT
                 for (int c = 0; c < 4; ++c) ov[c] *= rs * (a.xw ? a.xw[h * DV + 4 * cg + c] : 1.f);
             }
             const long long at = (static_cast<long long>(t) * a.Hv + h) * DV + 4 * cg;
-            if (a.out_bf16) {
+            const bool o_in = in_bounds(at + 3, static_cast<long long>(a.T) * a.Hv * DV, err);
+            if (o_in && a.out_bf16) {
                 __nv_bfloat162 lo = __floats2bfloat162_rn(ov[0], ov[1]), hi = __floats2bfloat162_rn(ov[2], ov[3]);
                 uint2 w;
                 w.x = *reinterpret_cast<const uint32_t *>(&lo);
                 w.y = *reinterpret_cast<const uint32_t *>(&hi);
                 *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at) = w;
-            } else {
+            } else if (o_in) {
                 st_global4(static_cast<float *>(a.o) + at, make_float4(ov[0], ov[1], ov[2], ov[3]));
             }
         }

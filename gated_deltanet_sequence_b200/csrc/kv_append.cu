@@ -97,7 +97,9 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
 }
 
 template <typename IT>
-__device__ __forceinline__ void store_codes(uint8_t *dst, const Chunk<IT> &c, float inv) {
+__device__ __forceinline__ void store_codes(uint8_t *cache, long long at, long long n, const Chunk<IT> &c, float inv,
+                                            unsigned *err) {
+    if (!in_bounds(at, n - 7, err)) return;
     float f[8];
     c.get(f);
 #pragma unroll
@@ -109,7 +111,7 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const Chunk<IT> &c, fl
     uint2 w;
     w.x = to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16);
     w.y = to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16);
-    *reinterpret_cast<uint2 *>(dst) = w;
+    *reinterpret_cast<uint2 *>(cache + at) = w;
 }
 
 // The scale of a run's block: fresh blocks take what the run needs, others the larger of that
@@ -153,6 +155,7 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
     const long long stride = z ? a.stride[1] : a.stride[0];
     uint8_t *cache = z ? a.cache[1] : a.cache[0];
     float *scale = z ? a.scale[1] : a.scale[0];
+    const long long ncodes = static_cast<long long>(nslots) * a.H * D;      // (bounds checks of the debug build)
 
     // slots of this block's rows and of the rows a run may reach past them; a bit where a run starts
     // (or a row that is skipped, or the end)
@@ -222,11 +225,11 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         for (int w = 1; w < kAppWarps; ++w) m = fmaxf(m, s_max[e & 1][w]);
         const float sc = run_scale(m, off == 0, old);
         const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
-        uint8_t *dst = cache + (bh << a.bs_log2) * D;
+        const long long blk0 = (bh << a.bs_log2) * D;          // the block's first code
 #pragma unroll
         for (int j = 0; j < STEPS; ++j)
-            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(dst + off * D + (tid + j * kAppThreads) * 8, c[j], inv);
-        if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, tid, kAppThreads);
+            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, err);
+        if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, tid, kAppThreads);
         // everyone has read the old scale: each did before the barrier above
         if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     }
@@ -251,13 +254,13 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float sc = run_scale(m, off == 0, old);
         const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
-        uint8_t *dst = cache + (bh << a.bs_log2) * D;
+        const long long blk0 = (bh << a.bs_log2) * D;          // the block's first code
 #pragma unroll
         for (int j = 0; j < kWarpSteps; ++j) {
             const int id = lane + j * 32;
-            if (id < len * CPR) store_codes(dst + off * D + id * 8, w[j], inv);
+            if (id < len * CPR) store_codes(cache, blk0 + off * D + id * 8, ncodes, w[j], inv, err);
         }
-        if (off > 0 && sc != old) rescale_codes(dst, off * D, old * inv, lane, 32);
+        if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, lane, 32);
         __syncwarp();
         if (lane == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     }

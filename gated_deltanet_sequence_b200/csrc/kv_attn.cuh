@@ -165,6 +165,7 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, long long token, in
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const bool none = l == 0.f;
     const long long at = (token * a.Hq + head) * d + x;
+    if (!in_bounds(at + N - 1, static_cast<long long>(a.T) * a.Hq * d, a.err)) return;
     if (a.out_bf16) {
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + at;
 #pragma unroll

@@ -688,7 +688,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                                                                        l == 0.f ? 0.f : o[i + 2 * k + 1] * inv);
                         w[k] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                    if (in) *reinterpret_cast<uint4 *>(op + 32 * ch + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (in && in_bounds((token * a.Hq + head) * D + 32 * ch + i + 7, static_cast<long long>(a.T) * a.Hq * D, a.err))
+                        *reinterpret_cast<uint4 *>(op + 32 * ch + i) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             if (in && a.lse) a.lse[token * a.Hq + head] = l == 0.f ? kNegInf : 0.6931471805599453f * (m + log2f(l));
@@ -707,6 +708,7 @@ gdn_status_t launch_t(const CUtensorMap &mk, const CUtensorMap &mv, const AttnAr
     const long long all = static_cast<long long>(a.T) * (a.Hq / a.Hkv);
     const long long units = (all / kUnitRows + std::min<long long>(a.N, all / a.many_rows)) * a.Hkv;
     if (units > 2147483647ll) return GDN_ERR_UNSUPPORTED;
+    if (units == 0) return GDN_OK;         // fewer rows in all than one such request has
     if (cudaMemsetAsync(redo, 0, static_cast<size_t>(a.N) * sizeof(int), stream) != cudaSuccess) return GDN_ERR_CUDA;
     kern<<<static_cast<unsigned>(units), kThreads, Lay<D>::kAlloc, stream>>>(mk, mv, a, redo);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -114,7 +114,8 @@ gdn_status_t gdn_kv_attn(const void *q, long long q_stride, const void *k_cache,
     while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
     a.max_blocks = max_blocks;
     a.max_q = max_q_len;
-    a.window = window;
+    // a window that no context outgrows is none
+    a.window = window >= static_cast<long long>(max_blocks) * block_size ? 0 : window;
     a.out_bf16 = out_dtype == GDN_BF16 ? 1 : 0;
     a.scale_log2 = scale * 1.4426950408889634f;
     return gdn::launch_kv_attn(k_cache, v_cache, a, d, in_dtype == GDN_F32, out_dtype == GDN_F32,

@@ -215,6 +215,8 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
         new.append(o)
     else:
         _want("o", o, (T, Hq, d), odt, dev)
+    if lse is False:
+        lse = None
     if lse is True:
         lse = q.new_empty((T, Hq), dtype=_f32)
         new.append(lse)

@@ -460,10 +460,17 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  workspace    device memory of at least gdn_kv_attn_workspace_bytes(...) bytes, 16-byte
  *               aligned, owned by the caller; contents irrelevant on entry and unspecified on
  *               return. Calls that may overlap on the GPU need one each.
- *  Sums and softmax statistics are fp32. bf16 queries enter the products exactly; fp32 ones as
- *  two fp16 parts (22 bits). The weights enter them as fp16 with a bf16 output, and as two
- *  fp16 parts with an fp32 one. A position that a query does not see does not reach its
- *  result, whatever its values.
+ *  Sums and softmax statistics are fp32. Queries are scaled by a power of two for each row and
+ *  enter the products as two fp16 parts (fp32 queries: 22 bits), as fp16 (bf16 queries, fp32
+ *  output: exact) or, with a bf16 output, as two e4m3 parts (bf16 queries: exact down to 2^-9
+ *  of the row's largest element, within 2^-17.8 of that element below). The weights enter as
+ *  fp16 with a bf16 output, and as two fp16 parts with an fp32 one. A position that a query
+ *  does not see does not reach its result, whatever its values; a NaN that it sees (append
+ *  stores infinities as NaN) makes its result NaN, a NaN of V in that column alone. Infinite
+ *  queries give NaN.
+ *  Requests of more than 64 rows (query tokens x query heads of a KV head) run on a tcgen05
+ *  kernel when q and o are bf16; all others, and fp32 in or out whatever the rows, on the
+ *  kernel for few rows, which reads the cache once for each 16 rows.
  *  N >= 1, T >= 0, 1 <= Hkv <= Hq, Hq % Hkv == 0, Hq <= 65535, d in {64, 128}, block_size in
  *  {16, 32, 64, 128}, window >= 0, scale finite; num_blocks * Hkv * block_size and max_blocks *
  *  block_size < 2^31; q, o, caches 16-byte aligned, the row stride of q a multiple of 16 bytes.

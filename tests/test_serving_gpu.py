@@ -111,7 +111,7 @@ def _plan_state(rng, ctx, bs, mb, spare):
 
 @pytest.mark.parametrize("n,hi,newhi,bs,spare,T_more", [
     (1, 40, 1, 16, 4, 0), (1, 0, 700, 16, 60, 3), (7, 100, 30, 32, 40, 5), (256, 300, 1, 64, 300, 0),
-    (300, 5, 90, 16, 2500, 0), (1500, 20, 3, 16, 3000, 1), (40, 100, 400, 128, 300, 77), (33, 2000, 2, 16, 3, 0),
+    (300, 5, 90, 16, 2500, 0), (1500, 20, 3, 16, 3000, 1), (8192, 3, 1, 16, 9000, 2), (40, 100, 400, 128, 300, 77), (33, 2000, 2, 16, 3, 0),
 ])
 def test_plan_matches_the_loop(S, lib, n, hi, newhi, bs, spare, T_more):
     rng = np.random.default_rng(n + bs)
@@ -512,6 +512,21 @@ def test_attn_takes_strided_queries_and_the_last_block_of_a_large_cache(S, lib):
     ro, rl, A, ds, _ = attn_ref(small, q, [[0]], [0, n], [n], 0, d ** -0.5)
     for got, ref, a, e in ((o.double().cpu()[0], ro[-1], A[-1], ds[-1]), (o2.double().cpu(), ro, A, ds)):
         assert ((got - ref).abs() <= 2.0 ** -24 * ref.abs() + a * (2 * e[..., None] + 2.0 ** -19)).all()
+
+
+@pytest.mark.parametrize("window", [0, 2 ** 31 - 1])
+def test_attn_bounds_far_above_the_batch(S, lib, window):
+    """max_q_len and the window are bounds: one row under a bound of thousands, a window that nothing outgrows."""
+    kv, ql = [30, 5], [1, 3]
+    cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, 64, 16, torch.bfloat16, seed=17)
+    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.125, torch.bfloat16)
+    a, l = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), scale=0.125, max_q_len=3, out_dtype=torch.bfloat16, lse=True)
+    b, none = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), scale=0.125, max_q_len=2 ** 31 - 1, window=window,
+                            out_dtype=torch.bfloat16, lse=False)
+    assert lib.gdn_sync_status() == 0 and torch.equal(a, b) and none is None
+    one, _ = S.gdn_kv_attn(cache, q[:1], tab[:1], i32([0, 1]), i32(kv[:1]), scale=0.125, max_q_len=4096, window=window,
+                           out_dtype=torch.bfloat16)
+    assert lib.gdn_sync_status() == 0 and torch.equal(one, a[:1])
 
 
 def test_attn_streams_graphs_and_two_calls_at_once(S, lib):
