@@ -40,6 +40,12 @@ template <> struct Chunk<__nv_bfloat16> {
     uint4 w;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+    // bits of the largest magnitude, as fp32 (NaN and infinities count)
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t m = 0x7fff7fffu;
+        const uint32_t t = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+        return max(t & 0xffff0000u, t << 16);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -56,21 +62,30 @@ template <> struct Chunk<float> {
         b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ uint32_t top() const {
+        float f[8];
+        get(f);
+        uint32_t t = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(f[i]) & 0x7fffffffu);
+        return t;
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
 };
 
-// largest finite magnitude
+// bits of the largest finite magnitude: for runs that hold NaN or an infinity, where top() says that
+constexpr uint32_t kInfBits = 0x7f800000u;
 template <typename IT>
-__device__ __forceinline__ float chunk_max(const Chunk<IT> &c) {
-    float f[8], m = 0.f;
+__device__ __noinline__ uint32_t finite_top(const Chunk<IT> &c) {
+    float f[8];
     c.get(f);
-#pragma unroll
+    uint32_t m = 0u;
     for (int i = 0; i < 8; ++i) {
-        const float x = fabsf(f[i]);
-        m = x < __int_as_float(0x7f800000) ? fmaxf(m, x) : m;
+        const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+        m = u < kInfBits ? max(m, u) : m;
     }
     return m;
 }
@@ -96,21 +111,22 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Codes of a chunk, at cache[at]; inv is a power of two, so the products are exact. odd: the run holds NaN or an
+// infinity; an infinity would be taken to 448 and is stored as NaN instead, so that it shows.
 template <typename IT>
-__device__ __forceinline__ void store_codes(uint8_t *cache, long long at, long long n, const Chunk<IT> &c, float inv,
+__device__ __forceinline__ void store_codes(uint8_t *cache, long long at, long long n, const Chunk<IT> &c, float inv, bool odd,
                                             unsigned *err) {
     if (!in_bounds(at, n - 7, err)) return;
     float f[8];
     c.get(f);
+    if (odd) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = f[i] * inv;      // exact: inv is a power of two
-        // an infinity would be taken to 448: it is stored as NaN instead, so that it shows
-        f[i] = fabsf(f[i]) == __int_as_float(0x7f800000) ? __int_as_float(0x7fffffff) : x;
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(f[i]) == __uint_as_float(kInfBits)) f[i] = __int_as_float(0x7fffffff);
     }
     uint2 w;
-    w.x = to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16);
-    w.y = to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16);
+    w.x = to_e4m3x2(f[0] * inv, f[1] * inv) | (to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
+    w.y = to_e4m3x2(f[4] * inv, f[5] * inv) | (to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
     *reinterpret_cast<uint2 *>(cache + at) = w;
 }
 
@@ -146,7 +162,7 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
     __shared__ int s_slot[kMaxRows + kMaxBs];
     __shared__ uint32_t s_brk[kMaskWords];
     __shared__ int s_long[kMaxRows], s_short[kMaxRows], s_nlong, s_nshort;
-    __shared__ float s_max[2][kAppWarps];
+    __shared__ uint32_t s_max[2][kAppWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h0 = blockIdx.y * a.HG, nh = min(a.HG, a.H - h0), z = blockIdx.z, bs = 1 << a.bs_log2;
     const long long r0 = static_cast<long long>(blockIdx.x) * a.R;
@@ -204,31 +220,43 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         }
     };
     Chunk<IT> c[STEPS], ahead[STEPS];
+    int turn = 0;
     if (nlong > 0) load_long(0, ahead);
     for (int e = 0; e < nlong; ++e) {
         const int run = s_long[e / nh], i0 = run & 255, len = run >> 8;
         const int slot = s_slot[i0], off = slot & (bs - 1);
         const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h0 + e % nh;
         const float old = off > 0 ? scale[bh] : 0.f;
-        float m = 0.f;
+        uint32_t m = 0u;
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) c[j] = ahead[j];
         if (e + 1 < nlong) load_long(e + 1, ahead);
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) m = fmaxf(m, chunk_max(c[j]));
+        for (int j = 0; j < STEPS; ++j) m = max(m, c[j].top());
+        auto block_max = [&](uint32_t x) {
+            x = __reduce_max_sync(0xffffffffu, x);
+            if (lane == 0) s_max[turn][warp] = x;
+            __syncthreads();      // (and the item before is through with the other s_max)
+            x = s_max[turn][0];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) s_max[e & 1][warp] = m;
-        __syncthreads();      // (and the item before is through with the other s_max)
-        m = s_max[e & 1][0];
+            for (int w = 1; w < kAppWarps; ++w) x = max(x, s_max[turn][w]);
+            turn ^= 1;
+            return x;
+        };
+        m = block_max(m);
+        const bool odd = m >= kInfBits;
+        if (odd) {                // rare: the scale goes by the finite ones
+            m = 0u;
 #pragma unroll
-        for (int w = 1; w < kAppWarps; ++w) m = fmaxf(m, s_max[e & 1][w]);
-        const float sc = run_scale(m, off == 0, old);
+            for (int j = 0; j < STEPS; ++j) m = max(m, finite_top(c[j]));
+            m = block_max(m);
+        }
+        const float sc = run_scale(__uint_as_float(m), off == 0, old);
         const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
         const long long blk0 = (bh << a.bs_log2) * D;          // the block's first code
 #pragma unroll
         for (int j = 0; j < STEPS; ++j)
-            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, err);
+            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, odd, err);
         if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, tid, kAppThreads);
         // everyone has read the old scale: each did before the barrier above
         if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
@@ -241,7 +269,7 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h;
         const float old = off > 0 ? scale[bh] : 0.f;
         Chunk<IT> w[kWarpSteps];
-        float m = 0.f;
+        uint32_t m = 0u;
 #pragma unroll
         for (int j = 0; j < kWarpSteps; ++j) {
             const int id = lane + j * 32;
@@ -249,16 +277,22 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
             else w[j].zero();
         }
 #pragma unroll
-        for (int j = 0; j < kWarpSteps; ++j) m = fmaxf(m, chunk_max(w[j]));
+        for (int j = 0; j < kWarpSteps; ++j) m = max(m, w[j].top());
+        m = __reduce_max_sync(0xffffffffu, m);
+        const bool odd = m >= kInfBits;
+        if (odd) {
+            m = 0u;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float sc = run_scale(m, off == 0, old);
+            for (int j = 0; j < kWarpSteps; ++j) m = max(m, finite_top(w[j]));
+            m = __reduce_max_sync(0xffffffffu, m);
+        }
+        const float sc = run_scale(__uint_as_float(m), off == 0, old);
         const float inv = exp2i(127 - static_cast<int>(__float_as_uint(sc) >> 23));
         const long long blk0 = (bh << a.bs_log2) * D;          // the block's first code
 #pragma unroll
         for (int j = 0; j < kWarpSteps; ++j) {
             const int id = lane + j * 32;
-            if (id < len * CPR) store_codes(cache, blk0 + off * D + id * 8, ncodes, w[j], inv, err);
+            if (id < len * CPR) store_codes(cache, blk0 + off * D + id * 8, ncodes, w[j], inv, odd, err);
         }
         if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, lane, 32);
         __syncwarp();
