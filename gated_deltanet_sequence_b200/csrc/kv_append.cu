@@ -124,10 +124,25 @@ __device__ __forceinline__ void store_codes(uint8_t *cache, long long at, long l
         for (int i = 0; i < 8; ++i)
             if (fabsf(f[i]) == __uint_as_float(kInfBits)) f[i] = __int_as_float(0x7fffffff);
     }
-    uint2 w;
-    w.x = to_e4m3x2(f[0] * inv, f[1] * inv) | (to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-    w.y = to_e4m3x2(f[4] * inv, f[5] * inv) | (to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-    *reinterpret_cast<uint2 *>(cache + at) = w;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint64_t x[2], y;                    // two-wide products
+        asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(inv));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x[k]) : "f"(f[4 * i + 2 * k]), "f"(f[4 * i + 2 * k + 1]));
+            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x[k]) : "l"(y));
+        }
+        // both pairs' codes into one word
+        asm("{\n\t.reg .f32 a, b, c, d;\n\t.reg .b16 p, q;\n\t"
+            "mov.b64 {a, b}, %1;\n\tmov.b64 {c, d}, %2;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 p, b, a;\n\tcvt.rn.satfinite.e4m3x2.f32 q, d, c;\n\t"
+            "mov.b32 %0, {p, q};\n\t}"
+            : "=r"(w[i])
+            : "l"(x[0]), "l"(x[1]));
+    }
+    *reinterpret_cast<uint2 *>(cache + at) = make_uint2(w[0], w[1]);
 }
 
 // The scale of a run's block: fresh blocks take what the run needs, others the larger of that
@@ -208,41 +223,43 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
     }
     __syncthreads();
 
-    // ---- long runs, head by head: the whole block
-    const int nlong = s_nlong * nh, nshort = s_nshort * nh;
-    auto load_long = [&](int e, Chunk<IT> (&c)[STEPS]) {
-        const int run = s_long[e / nh], i0 = run & 255, len = run >> 8;
-        const IT *row = x + (r0 + i0 + tid / CPR) * stride + (h0 + e % nh) * D + (tid % CPR) * 8;
+    // ---- long runs, head by head: the whole block. Items (run, head) in order; `it` holds an item's place.
+    struct Item {
+        int run, head;
+    };
+    const int nlong = s_nlong, nshort = s_nshort * nh;
+    auto next = [&](Item &it) {
+        if (++it.head == nh) {
+            it.head = 0;
+            ++it.run;
+        }
+    };
+    auto load_long = [&](const Item &it, Chunk<IT> (&c)[STEPS]) {
+        const int run = s_long[it.run], i0 = run & 255, len = run >> 8;
+        const IT *row = x + (r0 + i0 + tid / CPR) * stride + (h0 + it.head) * D + (tid % CPR) * 8;
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {
             if (tid / CPR + j * (kAppThreads / CPR) < len) c[j].load(row + j * (kAppThreads / CPR) * stride);
             else c[j].zero();
         }
     };
-    Chunk<IT> c[STEPS], ahead[STEPS];
     int turn = 0;
-    if (nlong > 0) load_long(0, ahead);
-    for (int e = 0; e < nlong; ++e) {
-        const int run = s_long[e / nh], i0 = run & 255, len = run >> 8;
+    auto block_max = [&](uint32_t v) {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (lane == 0) s_max[turn][warp] = v;
+        __syncthreads();      // (and the item before is through with the other s_max)
+        v = __reduce_max_sync(0xffffffffu, s_max[turn][lane & (kAppWarps - 1)]);
+        turn ^= 1;
+        return v;
+    };
+    auto code_long = [&](const Item &it, const Chunk<IT> (&c)[STEPS]) {
+        const int run = s_long[it.run], i0 = run & 255, len = run >> 8;
         const int slot = s_slot[i0], off = slot & (bs - 1);
-        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h0 + e % nh;
+        const long long bh = static_cast<long long>(slot >> a.bs_log2) * a.H + h0 + it.head;
         const float old = off > 0 ? scale[bh] : 0.f;
         uint32_t m = 0u;
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) c[j] = ahead[j];
-        if (e + 1 < nlong) load_long(e + 1, ahead);
-#pragma unroll
         for (int j = 0; j < STEPS; ++j) m = max(m, c[j].top());
-        auto block_max = [&](uint32_t x) {
-            x = __reduce_max_sync(0xffffffffu, x);
-            if (lane == 0) s_max[turn][warp] = x;
-            __syncthreads();      // (and the item before is through with the other s_max)
-            x = s_max[turn][0];
-#pragma unroll
-            for (int w = 1; w < kAppWarps; ++w) x = max(x, s_max[turn][w]);
-            turn ^= 1;
-            return x;
-        };
         m = block_max(m);
         const bool odd = m >= kInfBits;
         if (odd) {                // rare: the scale goes by the finite ones
@@ -256,10 +273,24 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         const long long blk0 = (bh << a.bs_log2) * D;          // the block's first code
 #pragma unroll
         for (int j = 0; j < STEPS; ++j)
-            if (tid / CPR + j * (kAppThreads / CPR) < len) store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, odd, err);
+            if (tid / CPR + j * (kAppThreads / CPR) < len)
+                store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, odd, err);
         if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, tid, kAppThreads);
         // everyone has read the old scale: each did before the barrier above
         if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
+    };
+    {
+        Chunk<IT> c[STEPS], ahead[STEPS];
+        Item it{0, 0};
+        if (nlong > 0) load_long(it, ahead);
+        while (it.run < nlong) {
+            const Item now = it;
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) c[j] = ahead[j];
+            next(it);
+            if (it.run < nlong) load_long(it, ahead);
+            code_long(now, c);
+        }
     }
 
     // ---- short runs: one, of one head, to a warp
