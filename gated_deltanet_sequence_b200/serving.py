@@ -32,6 +32,7 @@ _BLOCK_SIZES = (16, 32, 64, 128)
 # The calls below run once a layer and decoded token, on batches whose kernels take a few microseconds, so what they do
 # on the host is kept short: the raw stream handle where torch offers it, one comparison for a tensor that is right.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
 
 
@@ -53,10 +54,9 @@ def _used_on(stream, dev: torch.device, *tensors):
             t.record_stream(stream)
 
 
-def _call(fn: str, dev: torch.device, *args):
+def _call(f, fn: str, dev: torch.device, args) -> None:
     """One call of the library with ``dev`` current (it launches on the current device)."""
-    f = getattr(lib, fn)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _device_now():
         st = f(*args)
     else:
         with torch.cuda.device(dev):
@@ -150,11 +150,14 @@ def gdn_plan_batch(ctx_lens, new_lens, block_table, free_list, free_count, block
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected (N, max_blocks), got {tuple(block_table.shape)}")
     mb, nb = block_table.shape[1], free_list.numel()
-    for name, t, shape in (("ctx_lens", ctx_lens, (N,)), ("new_lens", new_lens, (N,)), ("block_table", block_table, (N, mb)),
-                           ("free_list", free_list, (nb,)), ("free_count", free_count, (1,))):
-        _want(name, t, shape, _i32, dev)
-    _call("gdn_plan_batch", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), N, block_table.data_ptr(), mb,
-          free_list.data_ptr(), free_count.data_ptr(), nb, block_size, plan.T, *plan._args, _stream_of(dev, stream))
+    _want("ctx_lens", ctx_lens, (N,), _i32, dev)
+    _want("new_lens", new_lens, (N,), _i32, dev)
+    _want("block_table", block_table, (N, mb), _i32, dev)
+    _want("free_list", free_list, (nb,), _i32, dev)
+    _want("free_count", free_count, (1,), _i32, dev)
+    _call(lib.gdn_plan_batch, "gdn_plan_batch", dev,
+          (ctx_lens.data_ptr(), new_lens.data_ptr(), N, block_table.data_ptr(), mb, free_list.data_ptr(),
+           free_count.data_ptr(), nb, block_size, plan.T, *plan._args, _stream_of(dev, stream)))
     return plan
 
 
@@ -167,8 +170,9 @@ def gdn_kv_append(cache: KvCache, k, v, slot_map, stream=None) -> KvCache:
     vs = _rows("v", v, shape, k.dtype, dev)
     _want("slot_map", slot_map, (T,), _i32, dev)
     kc, vc, kscale, vscale = cache._args
-    _call("gdn_kv_append", dev, k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), kc, vc, kscale, vscale, T,
-          cache.heads, cache.d, cache.num_blocks, cache.block_size, _lib._dtype_code(k), _stream_of(dev, stream))
+    _call(lib.gdn_kv_append, "gdn_kv_append", dev,
+          (k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), kc, vc, kscale, vscale, T, cache.heads, cache.d,
+           cache.num_blocks, cache.block_size, _lib._dtype_code(k), _stream_of(dev, stream)))
     return cache
 
 
@@ -229,10 +233,10 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     _used_on(stream, dev, *new)
     kc, vc, kscale, vscale = cache._args
-    _call("gdn_kv_attn", dev, q.data_ptr(), qs, kc, vc, kscale, vscale, block_table.data_ptr(), cu_seqlens.data_ptr(),
+    _call(lib.gdn_kv_attn, "gdn_kv_attn", dev, (q.data_ptr(), qs, kc, vc, kscale, vscale, block_table.data_ptr(), cu_seqlens.data_ptr(),
           kv_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), N, T, Hq, cache.heads, d, cache.num_blocks, cache.block_size, mb,
-          max_q_len, window, scale, dt, _lib.GDN_BF16 if odt is _bf16 else _lib.GDN_F32, raw)
+          max_q_len, window, scale, dt, _lib.GDN_BF16 if odt is _bf16 else _lib.GDN_F32, raw))
     return o, lse
 
 
@@ -255,10 +259,14 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
         raise ValueError(f"{Hv} value heads over {Hk} key heads")
     if beta is not None:
         _want("beta", beta, (T, Hv), _f32, dev)
-    vec = _lib._check_gate(g, (T, Hv), dk, dev)
+    vec = False
+    if g is not None:
+        vec = g.dim() == 3
+        _want("g", g, (T, Hv, dk) if vec else (T, Hv), _f32, dev)
     if state.dim() != 4:
         raise ValueError(f"state: expected (n_slots, Hv, dk, dv), got {tuple(state.shape)}")
-    _want("state", state, (state.shape[0], Hv, dk, dv), _f32, dev)
+    n_slots = state.shape[0]
+    _want("state", state, (n_slots, Hv, dk, dv), _f32, dev)
     N = slots.numel()
     _want("slots", slots, (N,), _i32, dev)
     if cu_seqlens is None:
@@ -266,7 +274,10 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
             raise ValueError(f"{T} rows for {N} slots: give cu_seqlens")
     else:
         _want("cu_seqlens", cu_seqlens, (N + 1,), _i32, dev)
-    odt, opts = _out_opts(o, out_dtype, d_skip, Hv, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
+    if o is None and not vec and d_skip is None and xnorm is None and xnorm_weight is None and out_dtype in (None, _f32):
+        odt, opts = _f32, None
+    else:
+        odt, opts = _out_opts(o, out_dtype, d_skip, Hv, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
     if o is None:
@@ -274,8 +285,8 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
         _used_on(stream, dev, o)
     else:
         _want("o", o, (T, Hv, dv), odt, dev)
-    _call("gdn_decode_slots", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+    _call(lib.gdn_decode_slots, "gdn_decode_slots", dev, (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
           None if beta is None else beta.data_ptr(), None if g is None else g.data_ptr(), state.data_ptr(),
           slots.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(), N, T, Hk, Hv,
-          state.shape[0], dk, dv, scale, dt, None if opts is None else ctypes.byref(opts), raw)
+          n_slots, dk, dv, scale, dt, None if opts is None else ctypes.byref(opts), raw))
     return o
