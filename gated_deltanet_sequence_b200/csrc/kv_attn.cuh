@@ -23,6 +23,7 @@ struct AttnArgs {
     int N, T, Hq, Hkv, num_blocks, bs, bs_log2, max_blocks, max_q, window, out_bf16;
     float scale_log2;          // scale * log2(e): scores are kept as base-2 exponents
     int whole;                 // units are not cut (and not joined)
+    int cluster, blocks;       // blocks of a unit (1: shares of the line instead), and of the launch then
     // requests of more rows than this belong to the many-rows kernel (0: it is not used), but for those it left
     int many_rows;
     const int *redo;           // (N), nullable: requests that the many-rows kernel left
@@ -63,7 +64,7 @@ __device__ __forceinline__ ReqWork request_work(const AttnArgs &a, int n, bool m
     w.tile0 = 0;
     if (a.window > 0) w.tile0 = static_cast<int>(max(0ll, static_cast<long long>(w.kv) - w.qlen - a.window + 1) / 128);
     w.tiles = max(1, (w.kv + 127) / 128 - w.tile0);
-    w.work = static_cast<long long>(a.Hkv) * w.row_tiles * (w.tiles + kUnitCost);
+    w.work = static_cast<long long>(a.Hkv) * w.row_tiles * (a.cluster > 1 ? 1 : w.tiles + kUnitCost);
     w.bad = bad;
     return w;
 }
