@@ -14,7 +14,10 @@
 //
 // What bounds it: per tile and group the two products take 1024 cycles of the tensor pipe and the 16384
 // exponentials 1024 of the special-function units, so the two groups' softmax and products are interleaved:
-// one group's exponentials run under the other's products.
+// one group's exponentials run under the other's products. Four requests of 1000 to 2048 rows over 2048 to
+// 6000 tokens, 32 query and 8 KV heads, d = 128 (428 GFLOP): 500 to 514 us, 850 TFLOP/s; the few-rows
+// kernel takes 3417 us. A half tile takes 2200 cycles, of which 950 are waits, votes and tensor-memory
+// turnarounds and 1270 the weights; neither pipe is the limit (without the exponentials 459 us).
 //
 // Warps: 0 K tiles and scales, 1-2 UMMA issue (2: tensor memory too), 3 V tiles, 4-7 V conversion, 8-11 and 12-15 the groups.
 // Tensor memory: S (and P over it) of each group, O of each group, 512 columns at d = 128.
