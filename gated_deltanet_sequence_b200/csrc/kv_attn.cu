@@ -826,7 +826,7 @@ size_t kv_attn_ws_bytes(int N, int d) {
 // kv_prompt.cu: requests of more than a.many_rows rows (bf16 in and out); redo: (N) ints, zeroed by it
 gdn_status_t launch_kv_prompt(const void *kc, const void *vc, const AttnArgs &a, int d, int *redo, cudaStream_t stream);
 
-constexpr int kManyRows = 64;
+constexpr int kManyRows = 64, kManyRowsPerSm128 = 40, kManyRowsPerSm64 = 58;
 constexpr int kWholeTokens = 256, kWholeTokensMany = 1024;
 constexpr int kClusterTokens = 8 * kTile;
 
@@ -840,7 +840,7 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, kc, rows, d, std::min(a.bs, kStep)) || !make_cache_map(&mv, vc, rows, d, std::min(a.bs, kStep)))
         return GDN_ERR_CUDA;
-    const int grid = kv_attn_grid(d);
+    const int grid = kv_attn_grid(d), sms = grid / (d == 128 ? Smem<128>::kBlocks : Smem<64>::kBlocks);
     a.cuts = reinterpret_cast<CutUnit *>(a.ws + grid * 2 * part_floats(d));
     // Contexts (or windows) that the table bounds to kWholeTokens are not cut, nor those up to kWholeTokensMany where there
     // are units for half the blocks: no join, and fewer units begun (8 KV heads, d = 128, cut / not cut: one request of
@@ -856,7 +856,6 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
     a.cluster = 1;
     if (seen > kTile && seen <= kClusterTokens && static_cast<long long>(a.max_q) * (a.Hq / a.Hkv) <= kManyRows) {
         const long long units = (static_cast<long long>(a.T) * (a.Hq / a.Hkv) / kRows + a.N) * a.Hkv;      // at most
-        const int sms = grid / (d == 128 ? Smem<128>::kBlocks : Smem<64>::kBlocks);
         if (8 * units <= sms) {
             a.cluster = 8;
             a.blocks = static_cast<int>(8 * units);
@@ -865,7 +864,13 @@ gdn_status_t launch_kv_attn(const void *kc, const void *vc, AttnArgs a, int d, b
     int *redo = reinterpret_cast<int *>(a.cuts + grid);
     a.redo = redo;
     a.many_rows = 0;
-    if (!in_f32 && !out_f32 && static_cast<long long>(a.max_q) * (a.Hq / a.Hkv) > kManyRows) {
+    // The many-rows kernel walks a context with one block per 256 rows, this one spreads it over the device: the former pays
+    // from rows for a good part of the SMs on (at one token from each other request, the most that the prompts can have).
+    // Many / few rows, one prompt: d = 128, 4096 rows 40 / 30 us over 1024 tokens and 88 / 68 over 4096, 8192 rows 40 / 48
+    // and 89 / 118; d = 64, 8192 rows 35 / 33 and 82 / 80, 16384 rows 36 / 52 and 84 / 145.
+    const long long prompt_rows = static_cast<long long>(a.T - std::min(a.T, a.N - 1)) * a.Hq;
+    if (!in_f32 && !out_f32 && static_cast<long long>(a.max_q) * (a.Hq / a.Hkv) > kManyRows &&
+        prompt_rows >= static_cast<long long>(sms) * (d == 128 ? kManyRowsPerSm128 : kManyRowsPerSm64)) {
         a.many_rows = kManyRows;
         const gdn_status_t st = launch_kv_prompt(kc, vc, a, d, redo, stream);
         if (st != GDN_OK) return st;

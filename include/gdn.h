@@ -469,8 +469,10 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  stores infinities as NaN) makes its result NaN, a NaN of V in that column alone. Infinite
  *  queries give NaN.
  *  Requests of more than 64 rows (query tokens x query heads of a KV head) run on a tcgen05
- *  kernel when q and o are bf16; all others, and fp32 in or out whatever the rows, on the
- *  kernel for few rows, which reads the cache once for each 16 rows.
+ *  kernel when q and o are bf16 and the batch may hold prompts of thousands of rows: (T - N + 1)
+ *  * Hq of 40 (d = 128) or 58 (d = 64) rows for each SM, max_q_len * Hq / Hkv above 64. All
+ *  others run on the kernel for few rows, which reads the cache once for each 16 rows. Both hold
+ *  the bounds above.
  *  N >= 1, T >= 0, 1 <= Hkv <= Hq, Hq % Hkv == 0, Hq <= 65535, d in {64, 128}, block_size in
  *  {16, 32, 64, 128}, window >= 0, scale finite; num_blocks * Hkv * block_size and max_blocks *
  *  block_size < 2^31; q, o, caches 16-byte aligned, the row stride of q a multiple of 16 bytes.

@@ -370,11 +370,16 @@ def attn_case(S, kv, ql, Hkv, G, d, bs, dtype, seed, fill=None, spare=2):
     return cache, q, table, tab, cu
 
 
-def attn_check(S, lib, cache, q, table, tab, cu, kv, window, scale, out, max_q=None):
+def behind(q, rows, value=float("nan")):
+    """q and rows that belong to nobody behind it."""
+    return torch.cat([q, torch.full((rows, *q.shape[1:]), value, dtype=q.dtype, device=DEV)])
+
+
+def attn_check(S, lib, cache, q, table, tab, cu, kv, window, scale, out, max_q=None, pad=3):
     T = q.shape[0]
-    o = torch.full((T + 3, q.shape[1], q.shape[2]), 7.0, dtype=out, device=DEV)
-    lse = torch.full((T + 3, q.shape[1]), 7.0, device=DEV)
-    qq = torch.cat([q, torch.full((3, *q.shape[1:]), float("nan"), dtype=q.dtype, device=DEV)])     # rows of nobody
+    o = torch.full((T + pad, q.shape[1], q.shape[2]), 7.0, dtype=out, device=DEV)
+    lse = torch.full((T + pad, q.shape[1]), 7.0, device=DEV)
+    qq = behind(q, pad)
     mq = max_q or max([1] + [b - a for a, b in zip(cu, cu[1:])])
     S.gdn_kv_attn(cache, qq, tab, i32(cu), i32(kv), max_q_len=mq, window=window, scale=scale, o=o, lse=lse)
     assert lib.gdn_sync_status() == 0
@@ -570,7 +575,10 @@ def test_attn_gives_up_on_a_wait_and_reports_it(S, lib):
     assert lib.gdn_sync_status() == 0 and torch.equal(o, ref)
 
 
-PROMPT = {  # kv lengths, query rows: requests of more than 64 rows (tokens x heads of a KV head) take the many-rows kernel
+# A batch for thousands of rows gives its requests of more than 64 rows (tokens x heads of a KV head) to the many-rows
+# kernel, whether its rows are used or lie behind the last request: MANY rows behind make small batches take it.
+MANY = 9000
+PROMPT = {  # kv lengths, query rows
     "just over": ([65], [65]),
     "one tile": ([128], [128]),
     "ragged": ([300, 5, 131, 257], [300, 1, 67, 129]),
@@ -585,14 +593,26 @@ PROMPT = {  # kv lengths, query rows: requests of more than 64 rows (tokens x he
     (1, 1, 128, 64, 0, 0.09), (2, 4, 128, 16, 0, 0.09), (1, 3, 64, 32, 0, 0.125), (2, 1, 64, 128, 100, 0.125),
     (1, 2, 128, 128, 1, -0.09), (1, 8, 64, 16, 300, 0.125), (1, 1, 128, 32, 64, 0.0),
 ])
-def test_attn_prompts_match_fp64(S, lib, case, Hkv, G, d, bs, window, scale):
+@pytest.mark.parametrize("pad", [3, MANY])
+def test_attn_prompts_match_fp64(S, lib, case, Hkv, G, d, bs, window, scale, pad):
     kv, ql = PROMPT[case]
     args = attn_case(S, kv, ql, Hkv, G, d, bs, torch.bfloat16, seed=len(case) + d + bs, fill=0x7f)
-    attn_check(S, lib, *args, kv, window, scale, torch.bfloat16)
+    attn_check(S, lib, *args, kv, window, scale, torch.bfloat16, pad=pad)
 
 
+def test_attn_prompts_of_thousands_of_rows(S, lib):
+    """No rows behind: 9600 rows, then around the 5920 (40 for each of 148 SMs) that the many-rows kernel begins at."""
+    kv, ql = [420, 60], [290, 10]
+    args = attn_case(S, kv, ql, 8, 4, 128, 64, torch.bfloat16, seed=3)
+    attn_check(S, lib, *args, kv, 0, 0.09, torch.bfloat16, pad=0)
+    for m in (184, 185, 186):
+        args = attn_case(S, [m], [m], 8, 4, 128, 64, torch.bfloat16, seed=m)
+        attn_check(S, lib, *args, [m], 0, 0.09, torch.bfloat16, pad=0)
+
+
+@pytest.mark.parametrize("pad", [3, MANY])
 @pytest.mark.parametrize("d,bs", [(128, 16), (64, 64)])
-def test_attn_prompt_scales_far_apart(S, lib, d, bs):
+def test_attn_prompt_scales_far_apart(S, lib, d, bs, pad):
     """V scales of neighbouring blocks 2^40 apart (fp16 cannot hold them together), blocks of zeros, queries of 1e-20."""
     kv, ql = [300, 90], [150, 80]
     cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, d, bs, torch.bfloat16, seed=31)
@@ -600,17 +620,19 @@ def test_attn_prompt_scales_far_apart(S, lib, d, bs):
     for c, sc in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
         c.view(torch.uint8)[zero] = 0
         sc[zero] = 2.0 ** -100
-    attn_check(S, lib, cache, (q.float() * 1e-20).bfloat16(), table, tab, cu, kv, 0, 1e19, torch.bfloat16)
-    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.1, torch.bfloat16)
+    attn_check(S, lib, cache, (q.float() * 1e-20).bfloat16(), table, tab, cu, kv, 0, 1e19, torch.bfloat16, pad=pad)
+    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.1, torch.bfloat16, pad=pad)
     cache.v_scale.copy_(torch.exp2(torch.randint(-30, 10, cache.v_scale.shape, generator=_gen(1), device=DEV).float()))
-    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.5, torch.bfloat16)
+    attn_check(S, lib, cache, q, table, tab, cu, kv, 0, 0.5, torch.bfloat16, pad=pad)
 
 
+@pytest.mark.parametrize("pad", [0, MANY])
 @pytest.mark.parametrize("where", ["k", "v"])
 @pytest.mark.parametrize("window", [0, 50])
-def test_attn_prompt_nan_reaches_the_rows_that_see_it(S, lib, where, window):
+def test_attn_prompt_nan_reaches_the_rows_that_see_it(S, lib, where, window, pad):
     kv, ql, Hkv, G, d, bs = [200, 150], [120, 150], 2, 1, 64, 16
     cache, q, table, tab, cu = attn_case(S, kv, ql, Hkv, G, d, bs, torch.bfloat16, seed=78)
+    q = behind(q, pad)
     at = 133
     hole = cache.k if where == "k" else cache.v
     hole.view(torch.uint8)[table[0][at // bs], 1, at % bs, 9] = 0xff
@@ -623,13 +645,14 @@ def test_attn_prompt_nan_reaches_the_rows_that_see_it(S, lib, where, window):
         assert not bad[i, 0].any() and bool(bad[i, 1, 9]) == hit and bool(bad[i, 1].any()) == hit, i
         if where == "v":
             assert int(bad[i, 1].sum()) == int(hit)
-    assert not bad[cu[1]:].any()
+    assert not bad[cu[1]:cu[2]].any()
 
 
 def test_attn_prompt_bad_pages_graphs_and_waits(S, lib):
     kv, ql = [400, 30, 300], [400, 1, 90]
     cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, 128, 64, torch.bfloat16, seed=14)
-    cu_t, kv_t = i32(cu), i32(kv)
+    q = behind(q, MANY, 0.0)
+    cu_t, kv_t, n = i32(cu), i32(kv), cu[-1]
     kw = dict(max_q_len=400, scale=0.09, out_dtype=torch.bfloat16)
     good, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
     assert lib.gdn_sync_status() == 0
@@ -638,13 +661,13 @@ def test_attn_prompt_bad_pages_graphs_and_waits(S, lib):
         t2[0, 2] = b
         o, _ = S.gdn_kv_attn(cache, q, t2, cu_t, kv_t, **kw)
         assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG and lib.gdn_sync_status() == 0
-        assert torch.equal(o[:128], good[:128]) and torch.equal(o[400:], good[400:]) and torch.isfinite(o).all()
+        assert torch.equal(o[:128], good[:128]) and torch.equal(o[400:n], good[400:n]) and torch.isfinite(o[:n]).all()
         assert not torch.equal(o[128:400], good[128:400])
     # a request with more rows than max_q_len says is left out, by both kernels
     o = torch.full_like(good, 7.0)
     S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, max_q_len=100, scale=0.09, o=o)
     assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG
-    assert (o[:400] == 7).all() and torch.equal(o[400:], good[400:])
+    assert (o[:400] == 7).all() and torch.equal(o[400:n], good[400:n]) and (o[n:] == 7).all()
     # captured and replayed with other lengths; two streams at once
     o = torch.zeros_like(good)
     graph = torch.cuda.CUDAGraph()
@@ -654,12 +677,12 @@ def test_attn_prompt_bad_pages_graphs_and_waits(S, lib):
     torch.cuda.synchronize()
     outs = [S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, stream=st, **kw)[0] for st in side for _ in range(3)]
     torch.cuda.synchronize()
-    assert all(torch.equal(x, good) for x in outs)
+    assert all(torch.equal(x[:n], good[:n]) for x in outs)
     kv_t.copy_(i32([390, 30, 299]))
     graph.replay()
     torch.cuda.synchronize()
     want, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
-    assert torch.equal(o, want) and not torch.equal(o, good) and lib.gdn_sync_status() == 0
+    assert torch.equal(o[:n], want[:n]) and not torch.equal(o[:n], good[:n]) and lib.gdn_sync_status() == 0
     lib.gdn_set_wait_limit_for_testing(1)
     try:
         S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
@@ -669,7 +692,7 @@ def test_attn_prompt_bad_pages_graphs_and_waits(S, lib):
     finally:
         lib.gdn_set_wait_limit_for_testing(0)
     o, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, **kw)
-    assert torch.equal(o, want) and lib.gdn_sync_status() == 0
+    assert torch.equal(o[:n], want[:n]) and lib.gdn_sync_status() == 0
 
 
 # ---------------------------------------------------------------- recurrence over slots
