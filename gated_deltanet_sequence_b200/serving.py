@@ -45,13 +45,22 @@ def _stream_of(dev: torch.device, stream) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _used_on(stream, dev: torch.device, *tensors):
-    """Tensors made here on the current stream and used on ``stream``: kept until that is through with them."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        for t in tensors:
-            t.record_stream(stream)
+def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream, result: bool = True) -> torch.Tensor:
+    """A tensor made on the stream that the call uses: what torch hands out on another one may be memory that work queued
+    there still reads or writes. A result made on a passed stream is read on the current one (by a caller who waits),
+    so it is kept until that is through with it too."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    dev = like.device
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)      # (0 is the default stream, which ExternalStream does not take)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if result and here != stream:
+        t.record_stream(here)
+    return t
 
 
 def _call(f, fn: str, dev: torch.device, args) -> None:
@@ -213,25 +222,20 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
     need = gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, max_q_len)
-    new = []
     if o is None:
-        o = q.new_empty((T, Hq, d), dtype=odt)
-        new.append(o)
+        o = _new(q, (T, Hq, d), odt, stream)
     else:
         _want("o", o, (T, Hq, d), odt, dev)
     if lse is False:
         lse = None
     if lse is True:
-        lse = q.new_empty((T, Hq), dtype=_f32)
-        new.append(lse)
+        lse = _new(q, (T, Hq), _f32, stream)
     elif lse is not None:
         _want("lse", lse, (T, Hq), _f32, dev)
     if workspace is None:
-        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
-        new.append(workspace)
+        workspace = _new(q, max(need, 16), torch.uint8, stream, result=False)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _used_on(stream, dev, *new)
     kc, vc, kscale, vscale = cache._args
     _call(lib.gdn_kv_attn, "gdn_kv_attn", dev, (q.data_ptr(), qs, kc, vc, kscale, vscale, block_table.data_ptr(), cu_seqlens.data_ptr(),
           kv_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
@@ -281,8 +285,7 @@ def gdn_decode_slots(q, k, v, beta, g, state, slots, cu_seqlens=None, o=None, sc
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
     if o is None:
-        o = q.new_empty((T, Hv, dv), dtype=odt)
-        _used_on(stream, dev, o)
+        o = _new(q, (T, Hv, dv), odt, stream)
     else:
         _want("o", o, (T, Hv, dv), odt, dev)
     _call(lib.gdn_decode_slots, "gdn_decode_slots", dev, (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
