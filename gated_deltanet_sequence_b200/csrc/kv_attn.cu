@@ -16,7 +16,8 @@
 // (queries as two e4m3 parts), and go to fp16 in registers otherwise (e4m3 fits fp16 exactly; queries
 // as one or two fp16 parts); V's always do. The block scale, a power of two, multiplies the scores in
 // fp32; V's is carried as the unit of the accumulators (O is kept in units of the current block's V
-// scale and multiplied by the ratio, exactly, when it changes), so no operand is rounded for it.
+// scale and multiplied by the ratio, exactly, when it changes, down to 2^-64 of the largest), so no operand is
+// rounded for it.
 // Queries are divided by a power of two for each row so that the parts hold them. The weights are
 // one fp16 part, and two where the output is fp32.
 //
@@ -131,6 +132,7 @@ struct Worker {
     float m[2], l[2], rf[2];       // rows g and g + 8: reference of the exponents, this lane's part of the sum, score factor
     int hi[2], lo[2];              // positions a row sees: lo .. hi
     float vu;                      // V scale that the accumulators are in units of (0: none yet)
+    float floor;                   // the smallest unit they may fall to (see enter)
     bool saw_nan;                  // a NaN of V was taken out of an edge step
 
     __device__ __forceinline__ static int token_of(int n) { return D == 128 ? (n & 1) * 4 + (n >> 1) : n; }
@@ -140,6 +142,16 @@ struct Worker {
         for (int i = 0; i < NT; ++i) {
             o[i][0] *= f0; o[i][1] *= f0; o[i][2] *= f1; o[i][3] *= f1;
         }
+    }
+
+    // The accumulators' unit becomes that of a block of V scale vs; returned is the factor that they need for it. The unit
+    // never falls more than 2^64 below the largest scale met (floor), so that sums of 2^40 in units of that one stay
+    // finite: a block of zeros has the scale 2^-100. Nor does it fall below 2^-100, the smallest that append makes. What
+    // a smaller scale lacks goes into its block's weights (step).
+    __device__ __forceinline__ float enter(float vs) {
+        const float unit = fmaxf(vs, floor), f = vu == 0.f ? 1.f : vu / unit;
+        vu = unit;
+        return f;
     }
 
     // Queries of row g + 8 r from this lane's D / 4 coordinates (lane c: coordinates 16 (c + 4 half) + 0 .. 15).
@@ -276,7 +288,10 @@ struct Worker {
         for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
         // the accumulators' factors: of the references, and of V's unit
         float f[2] = {1.f, 1.f};
-        const bool move = __any_sync(0xffffffffu, top > kSlack || none[0] || none[1]);
+#pragma unroll
+        for (int b = 0; b < HV; ++b) floor = fmaxf(floor, vs[b] * 0x1p-64f);
+        const bool far = vs[0] < floor || vs[HV - 1] < floor;
+        const bool move = __any_sync(0xffffffffu, top > kSlack || none[0] || none[1] || far);
         if (move) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -293,11 +308,21 @@ struct Worker {
                 }
                 l[r] *= f[r];
             }
+            if (far) {      // rare: weights smaller by what the unit does not hold, but whole in the rows' sums
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float s = vs[HV == 1 ? 0 : j >> 1], lack = s < floor ? log2f(s) - log2f(floor) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        l[i >> 1] += ex2(x[j][i]) - ex2(x[j][i] + lack);
+                        x[j][i] += lack;
+                    }
+                }
+            }
         }
         if (move || vs[0] != vu) {
-            const float u = vu == 0.f ? 1.f : vu / vs[0];
+            const float u = enter(vs[0]);
             scale_o(f[0] * u, f[1] * u);
-            vu = vs[0];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -310,8 +335,8 @@ struct Worker {
         for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
             if constexpr (HV == 2) {
                 if (hf == 1 && vs[1] != vu) {
-                    scale_o(vu / vs[1], vu / vs[1]);
-                    vu = vs[1];
+                    const float u = enter(vs[1]);
+                    scale_o(u, u);
                 }
             }
             uint32_t p[4], pl[4];
@@ -535,6 +560,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
         for (int i = 0; i < W::NT; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
         w.vu = 0.f;
+        w.floor = 0x1p-100f;
         w.saw_nan = false;
 
         const int lo_last = a.window > 0 ? p_last - a.window + 1 : 0;

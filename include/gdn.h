@@ -464,7 +464,10 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  enter the products as two fp16 parts (fp32 queries: 22 bits), as fp16 (bf16 queries, fp32
  *  output: exact) or, with a bf16 output, as two e4m3 parts (bf16 queries: exact down to 2^-9
  *  of the row's largest element, within 2^-17.8 of that element below). The weights enter as
- *  fp16 with a bf16 output, and as two fp16 parts with an fp32 one. A position that a query
+ *  fp16 with a bf16 output, and as two fp16 parts with an fp32 one. V scales of a request's
+ *  blocks may be any powers of two apart; from 2^64 below the largest on, a block's values
+ *  enter with what is missing in their weights (lost where those fall below fp16's 2^-25). A
+ *  position that a query
  *  does not see does not reach its result, whatever its values; a NaN that it sees (append
  *  stores infinities as NaN) makes its result NaN, a NaN of V in that column alone. Infinite
  *  queries give NaN.

@@ -65,3 +65,81 @@ def test_the_default_stream_by_its_handle(S, lib):
     a = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), scale=0.125, lse=True)
     b = S.gdn_kv_attn(cache, q, tab, i32(cu), i32(kv), scale=0.125, lse=True, stream=0)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and lib.gdn_sync_status() == 0
+
+
+# ---------------------------------------------------------------- V's block scales
+def unit_case(S, scales, n, Hkv, G, d, bs, dtype, seed, positive=True, ql=1):
+    """One request of n tokens whose blocks' V scales go through `scales` in turn (a block of zeros where that is None),
+    V of one sign, so that sums grow with the tokens."""
+    cache, q, table, tab, cu = attn_case(S, [n], [ql], Hkv, G, d, bs, dtype, seed)
+    v = cache.v.float()
+    if positive:
+        cache.v.copy_(v.abs().clamp(min=1.0).to(cache.v.dtype))
+    for i, b in enumerate(table[0]):
+        e = scales[i % len(scales)]
+        if e is None:
+            cache.v.view(torch.uint8)[b] = 0
+        cache.v_scale[b] = 2.0 ** (-100 if e is None else e)
+    return cache, q, table, tab, cu
+
+
+UNITS = {  # exponents of V's block scales; None: a block of zeros
+    "zeros behind 2^20": [20, None, None],
+    "zeros behind 2^40": [40, None, None],
+    "zeros first": [None, None, 30, None, -20],
+    "falling": [90, 60, 30, 0, -30, -60, -90],
+    "rising": [-90, -30, 30, 90],
+    "both ends": [100, -100, 20, -100],
+}
+
+
+@pytest.mark.parametrize("case", list(UNITS))
+@pytest.mark.parametrize("n,bs,d,dtype,out", [
+    (4000, 64, 128, torch.bfloat16, torch.bfloat16), (4000, 16, 128, torch.bfloat16, torch.float32),
+    (700, 16, 64, torch.float32, torch.float32), (3000, 32, 64, torch.float32, torch.bfloat16),
+    (200, 16, 64, torch.bfloat16, torch.bfloat16), (2500, 128, 128, torch.float32, torch.float32)])
+def test_attn_v_scales_of_the_whole_range(S, lib, case, n, bs, d, dtype, out):
+    """gdn_kv_append makes scales of 2^-100 (a block of zeros) to 2^120: sums in units of one block's scale must neither
+    overflow nor be lost when the next block's lies far below or above."""
+    cache, q, table, tab, cu = unit_case(S, UNITS[case], n, 2, 4, d, bs, dtype, seed=40)
+    attn_check(S, lib, cache, q, table, tab, cu, [n], 0, 0.02, out)
+
+
+@pytest.mark.parametrize("case", list(UNITS))
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 64)])
+def test_attn_prompt_v_scales_of_the_whole_range(S, lib, case, d, bs):
+    """The same where the many-rows kernel looks at the request first and leaves it."""
+    cache, q, table, tab, cu = unit_case(S, UNITS[case], 500, 2, 2, d, bs, torch.bfloat16, seed=41, ql=120)
+    attn_check(S, lib, cache, q, table, tab, cu, [500], 0, 0.02, torch.bfloat16, pad=9000)
+
+
+@pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                       (torch.float32, torch.float32), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("far", [40, 64, 80])
+def test_attn_small_values_beside_large_ones_without_weight(S, lib, far, dtype, out):
+    """Every other block holds values 2^far larger whose weights vanish (200 nats below): the result is the small
+    values' alone. Beyond 2^64 the small blocks' weights take the rest of the power of two, 2^-16 here: as fp16 they
+    are then within 2^-25 / 2^-16 = 2^-9 each of the largest weight, as two parts within 2^-21."""
+    n, bs, d = 1600, 16, 64
+    cache, q, table, tab, cu = unit_case(S, [far - 40, -40], n, 1, 4, d, bs, dtype, seed=42)
+    q.copy_(torch.where(q > 0, 1.0, -1.0))
+    q[:, 1:] = q[:, :1]                                       # one sign pattern: a key along it scores far below
+    big = torch.tensor(table[0][0::2], device=DEV)
+    k = cache.k.float()
+    k[big] = -448.0 * q[0, 0].float()
+    cache.k.copy_(k.to(cache.k.dtype))
+    cache.k_scale.fill_(2.0 ** -7)                            # scale 0.9: 0.9 * 64 * 3.5 = 201 below
+    scale = 0.9
+    cache.k_scale[torch.tensor(table[0][1::2], device=DEV)] = 2.0 ** -12
+    q0 = q.clone()
+    o, lse = S.gdn_kv_attn(cache, q0, tab, i32(cu), i32([n]), scale=scale, out_dtype=out, lse=True)
+    assert lib.gdn_sync_status() == 0
+    ro, rl, A, ds, vm = attn_ref(cache, q0, table, cu, [n], 0, scale, dtype == out == torch.bfloat16)
+    assert ro.abs().max() < 448 * 2.0 ** -40
+    rel = 2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -24
+    part = (2.0 ** -11 if out == torch.bfloat16 else 2.0 ** -22) + 2.0 ** -20
+    if far > 64:
+        part += 2.0 ** -9 if out == torch.bfloat16 else 2.0 ** -21
+    tol = rel * ro.abs() + A * (2 * ds[..., None] + part + n * 2.0 ** -23)
+    assert ((o.double().cpu() - ro).abs() <= tol).all()
+    assert ((lse.double().cpu() - rl).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()
