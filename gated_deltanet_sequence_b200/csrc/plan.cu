@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
         ngone += static_cast<int>(both >> 48);
     }
     if (tokens > a.T) {     // uniform: the step does not fit its token grid, so it brings none
+        __syncthreads();    // everyone's length is in s_kvmax
         if (tid == 0) { atomicOr(err, kErrBadSeqlens); s_kvmax = 0; }
         __syncthreads();
         tokens = 0;

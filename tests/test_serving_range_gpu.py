@@ -143,3 +143,43 @@ def test_attn_small_values_beside_large_ones_without_weight(S, lib, far, dtype, 
     tol = rel * ro.abs() + A * (2 * ds[..., None] + part + n * 2.0 ** -23)
     assert ((o.double().cpu() - ro).abs() <= tol).all()
     assert ((lse.double().cpu() - rl).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()
+
+
+# ---------------------------------------------------------------- plan
+def plan_call(S, lib, ctx, new, table, free, count, bs, T, ctx_of=None):
+    """gdn_plan_batch on lists; ctx_of: makes the cached lengths' tensor from the plan (the plan's own kv_lens)."""
+    p = S.BatchPlan.empty(len(ctx), T, DEV)
+    c = i32(ctx) if ctx_of is None else ctx_of(p).copy_(i32(ctx))
+    t, f, n = i32(table), i32(free), i32([count])
+    S.gdn_plan_batch(c, i32(new), t, f, n, bs, p)
+    st = lib.gdn_sync_status()
+    got = {k: getattr(p, k).tolist() for k in ("cu_seqlens", "kv_lens", "positions", "seq_ids", "slot_map", "info")}
+    got.update(table=t.tolist(), free=f.tolist())
+    assert n.item() == got["info"][3]
+    return got, st
+
+
+def plan_state(ctx, bs, mb, spare):
+    """Tables with the cached tokens' blocks, numbered in order, and a free list of the others."""
+    table, at = [], 0
+    for c in ctx:
+        k = -(-c // bs)
+        table.append(list(range(at, at + k)) + [-1] * (mb - k))
+        at += k
+    return table, list(range(at, at + spare)) + [-1] * at, spare
+
+
+@pytest.mark.parametrize("N", [33, 700, 3000])
+def test_plan_of_a_refused_step_has_its_lengths(S, lib, N):
+    """More tokens than the grid has rows: info[1] is the longest cached length, with nothing of the refused tokens in it,
+    whichever warp comes last (the long request is each warp's in turn)."""
+    bs, mb = 16, 20
+    for at in (0, 31, N // 2, N - 1):
+        ctx = [(7 * i) % 50 for i in range(N)]
+        new = [3] * N
+        ctx[at], new[at] = 10, 300
+        table, free, count = plan_state(ctx, bs, mb, 4)
+        want, bad = plan_ref(ctx, new, table, free, count, bs, 3 * N)
+        for _ in range(5):
+            got, st = plan_call(S, lib, ctx, new, table, free, count, bs, 3 * N)
+            assert bad and st == lib.GDN_ERR_INVALID_ARG and got == want and got["info"][1] == 49
