@@ -66,7 +66,7 @@ __device__ __forceinline__ void plan_token(const PlanArgs &a, const int *cu, int
     int n = -1, p = -1, slot = -1;
     if (t < total) {
         n = find_range(cu, a.N, t);
-        p = a.ctx[n] + (t - cu[n]);
+        p = a.kv[n] - (cu[n + 1] - t);
         const int b = a.table[static_cast<long long>(n) * a.max_blocks + (p >> a.bs_log2)];
         if (b >= 0 && b < a.num_blocks) slot = (b << a.bs_log2) + (p & ((1 << a.bs_log2) - 1));
         else if (b >= a.num_blocks || !may_be_short) atomicOr(err, kErrBadSeqlens);
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
     if (tid == 0) s_kvmax = 0;
     __syncthreads();
 
-    // ---- offsets: tokens and new table entries of each request
+    // ---- offsets: tokens and new table entries of each request. This is the only look at ctx: it may be kv itself (a step
+    // that takes its cached lengths from the plan of the one before), so what follows takes the new tokens off kv.
     long long tokens = 0;
     int entries = 0, ngone = 0;
     for (int base = 0; base < a.N; base += kPlanThreads) {
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
         tokens = 0;
         entries = 0;
         for (int n = tid; n < a.N; n += kPlanThreads) {
-            const bool fin = a.add[n] == -1;
-            const int c = fin ? 0 : min(max(a.ctx[n], 0), static_cast<int>(cap));
+            const int c = a.kv[n] > 0 ? a.kv[n] - a.add[n] : 0;      // (0: finished, out of range, or nothing cached or new)
             tok[n] = 0;
             blk[n] = 0;
             a.kv[n] = c;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
     // ---- new blocks come off it in the same order, all of them or none
     auto new_entry = [&](int i) {
         const int n = find_range(blk, a.N, i);
-        const int first = (a.ctx[n] + bs - 1) >> a.bs_log2;
+        const int first = (a.kv[n] - (tok[n + 1] - tok[n]) + bs - 1) >> a.bs_log2;
         return a.table + static_cast<long long>(n) * a.max_blocks + first + (i - blk[n]);
     };
     int want = 0, missing = 0;

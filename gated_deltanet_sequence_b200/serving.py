@@ -153,7 +153,8 @@ class BatchPlan:
 def gdn_plan_batch(ctx_lens, new_lens, block_table, free_list, free_count, block_size: int, plan: BatchPlan,
                    stream=None) -> BatchPlan:
     """Block tables, slot maps and packed offsets of a step from the requests' lengths (N,) int32: ctx_lens tokens
-    cached, new_lens tokens brought (0: waiting, -1: finished, its blocks are freed). Updates block_table
+    cached (``plan.kv_lens`` of the step before will do), new_lens tokens brought (0: waiting, -1: finished, its blocks are
+    freed). Updates block_table
     (N, max_blocks), free_list (num_blocks,) and free_count (1,) in place, fills ``plan`` and returns it."""
     dev, N = plan.device, plan.N
     if block_table.dim() != 2:

@@ -401,7 +401,8 @@ gdn_status_t gdn_chunk_fwd_host(const void *q, const void *k, const void *v, con
  *  T           rows of the step's token grid
  *  cu_seqlens  (N + 1) int32: packed offsets of the new tokens (as the *_varlen calls
  *              take them)                                                          written
- *  kv_lens     (N) int32: ctx_lens + new tokens (0 for a finished request)         written
+ *  kv_lens     (N) int32: ctx_lens + new tokens (0 for a finished request, or for one whose
+ *              lengths are out of range); may be ctx_lens itself                   written
  *  positions, seq_ids, slot_map  (T) int32: each row's position in its request, its
  *              request, and its cache row block * block_size + position % block_size; -1 in
  *              rows behind the last request                                        written

@@ -183,3 +183,40 @@ def test_plan_of_a_refused_step_has_its_lengths(S, lib, N):
         for _ in range(5):
             got, st = plan_call(S, lib, ctx, new, table, free, count, bs, 3 * N)
             assert bad and st == lib.GDN_ERR_INVALID_ARG and got == want and got["info"][1] == 49
+
+
+def test_plan_refuses_a_step_with_bad_lengths_too(S, lib):
+    """More tokens than rows, and among the requests some whose own lengths are out of range and a finished one."""
+    ctx, new = [5, 20, 70, -3, 9, 0], [30, -2, 5, 1, -1, 0]
+    table, free, count = plan_state([5, 20, 0, 0, 9, 0], 16, 4, 6)
+    want, bad = plan_ref(ctx, new, table, free, count, 16, 8)
+    got, st = plan_call(S, lib, ctx, new, table, free, count, 16, 8)
+    assert bad and st == lib.GDN_ERR_INVALID_ARG and got == want and got["kv_lens"] == [5, 0, 0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("N,top,bs", [(5, 3, 16), (300, 2, 32), (40, 400, 64), (2000, 9, 16)])
+def test_plan_takes_its_own_kv_lens_as_cached_lengths(S, lib, N, top, bs):
+    """A program that hands the plan's kv_lens on as the next step's cached lengths: the same tensor read and written."""
+    g = torch.Generator().manual_seed(N)
+    mb = -(-(40 + 8 * top) // bs) + 1
+    ctx = torch.randint(0, 41, (N,), generator=g).tolist()
+    table, free, count = plan_state(ctx, bs, mb, N * mb)
+    rows = N * top + 5                                       # N = 40: the tokens' own kernel; the others one block
+    p = S.BatchPlan.empty(N, rows, DEV)
+    p.kv_lens.copy_(i32(ctx))
+    t, f, c = i32(table), i32(free), i32([count])
+    for step in range(6):
+        new = torch.randint(0, top + 1, (N,), generator=g)
+        if step == 3:
+            new[torch.rand(N, generator=g) < 0.2] = -1
+        new = new.tolist()
+        want, bad = plan_ref(ctx, new, table, free, count, bs, rows)
+        S.gdn_plan_batch(p.kv_lens, i32(new), t, f, c, bs, p)
+        assert not bad and lib.gdn_sync_status() == 0
+        for k in ("cu_seqlens", "kv_lens", "positions", "seq_ids", "slot_map", "info"):
+            assert getattr(p, k).tolist() == want[k], (step, k)
+        assert t.tolist() == want["table"] and f.tolist() == want["free"]
+        ctx, table, free, count = want["kv_lens"], want["table"], want["free"], want["info"][3]
+    S.gdn_plan_batch(p.kv_lens, i32([top + 2] * N), t, f, c, bs, p)      # more tokens than rows: the lengths stay
+    assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG
+    assert p.kv_lens.tolist() == ctx and t.tolist() == table and p.info.tolist() == [0, max(ctx), 0, count]
