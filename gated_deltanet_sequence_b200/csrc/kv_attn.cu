@@ -193,7 +193,12 @@ struct Worker {
             for (int s = 0; s < KS; ++s) {
                 float y[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = f[4 * s + i] * inv;
+                for (int i = 0; i < 4; ++i) {
+                    y[i] = f[4 * s + i] * inv;
+                    // an infinite query shows as NaN (as two parts it does so by itself): scores of -inf alone would pass
+                    // for a row that sees nothing
+                    if (QK == kF16 && fabsf(y[i]) > 65504.f) y[i] = __int_as_float(0x7fffffff);
+                }
                 if constexpr (QK == kF16x2) {
                     split_h2(y[0], y[1], qa[s][r], ql[s][r]);
                     split_h2(y[2], y[3], qa[s][r + 2], ql[s][r + 2]);

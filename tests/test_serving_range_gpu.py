@@ -220,3 +220,28 @@ def test_plan_takes_its_own_kv_lens_as_cached_lengths(S, lib, N, top, bs):
     S.gdn_plan_batch(p.kv_lens, i32([top + 2] * N), t, f, c, bs, p)      # more tokens than rows: the lengths stay
     assert lib.gdn_sync_status() == lib.GDN_ERR_INVALID_ARG
     assert p.kv_lens.tolist() == ctx and t.tolist() == table and p.info.tolist() == [0, max(ctx), 0, count]
+
+
+# ---------------------------------------------------------------- queries that are not finite
+@pytest.mark.parametrize("dtype,out,pad", [(torch.bfloat16, torch.bfloat16, 0), (torch.bfloat16, torch.float32, 0),
+                                           (torch.float32, torch.float32, 0), (torch.float32, torch.bfloat16, 0),
+                                           (torch.bfloat16, torch.bfloat16, 9000)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_attn_of_a_query_that_is_not_finite_is_nan(S, lib, dtype, out, pad, sign, value):
+    """Whatever the signs of the codes it meets: with codes of one sign all scores are the same infinity, and a row whose
+    scores are all -inf must not pass for one that sees nothing. Rows that do see nothing stay 0."""
+    kv, ql, d = [150, 90, 2], [70, 1, 5], 64
+    cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 2, d, 16, dtype, seed=50)
+    k = cache.k.float()
+    k[..., 7] = sign * k[..., 7].abs().clamp(min=1.0)
+    cache.k.copy_(k.to(cache.k.dtype))
+    q[3, 1, 7] = q[70, 3, 7] = q[71, 0, 7] = q[74, 2, 7] = value       # (row 71 is before position 0)
+    want = torch.zeros(q.shape[:2], dtype=torch.bool)
+    want[3, 1] = want[70, 3] = want[74, 2] = True
+    n = q.shape[0]
+    o, lse = S.gdn_kv_attn(cache, behind(q, pad), tab, i32(cu), i32(kv), max_q_len=70, scale=0.125, out_dtype=out, lse=True)
+    assert lib.gdn_sync_status() == 0
+    assert torch.equal(torch.isnan(o[:n]).all(-1).cpu(), want) and torch.equal(torch.isnan(o[:n]).any(-1).cpu(), want)
+    assert torch.equal(torch.isnan(lse[:n]).cpu(), want)
+    assert (o[71:74] == 0).all() and (lse[71:74] == -math.inf).all()
