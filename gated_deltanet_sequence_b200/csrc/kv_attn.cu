@@ -45,7 +45,11 @@ constexpr int kStep = 32;                   // tokens of a warp's step
 constexpr int kTile = kStep * kWarps;       // tokens of a block's tile
 constexpr int kRows = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kSlack = 8.f;               // a row's exponents may pass its reference by this much
+// A row's reference is kBias below the largest exponent of the step that moves it, and its exponents may pass it by
+// kSlack: fp16 holds weights up to 2^15, and starts to lose the small ones 2^-14 below 1. With the weights that high
+// in its range, what is lost is below 2^-32 of the largest weight (one part) or 2^-44 (two).
+constexpr float kBias = 7.f, kSlack = 15.f, kDown = 0x1p-15f;      // kDown: 2^-kSlack
+constexpr float kLowPart = 4096.f;          // the second part of a weight is this much larger
 
 template <int D> struct Smem {
     static constexpr int kBlocks = D == 128 ? 2 : 3;         // blocks an SM holds (registers)
@@ -117,6 +121,14 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = pack_h2(x - f.x, y - f.y);
 }
+// a weight as two fp16 parts: hi + lo / kLowPart = x to 2^-23, and to 2^-37 below fp16's range. What is left of a weight
+// of up to 2^15 is at most 2^3, so lo is at most 2^15 too.
+__device__ __forceinline__ void split_weight(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = pack_h2((x - f.x) * kLowPart, (y - f.y) * kLowPart);
+}
 // How queries enter Q K^T. kF8: as two e4m3 parts (bf16 queries with a bf16 output: the codes of K are then an
 // operand as they are); kF16, kF16x2: as one or two fp16 parts, K's codes converted.
 enum QKind { kF8, kF16, kF16x2 };
@@ -151,6 +163,7 @@ struct Worker {
     __device__ __forceinline__ float enter(float vs) {
         const float unit = fmaxf(vs, floor), f = vu == 0.f ? 1.f : vu / unit;
         vu = unit;
+        floor = fmaxf(floor, vs * 0x1p-64f);
         return f;
     }
 
@@ -262,8 +275,8 @@ struct Worker {
             }
         }
         // Base-2 exponents against the row's reference m; elements 0, 1: row g, tokens token_of(2c), token_of(2c + 1),
-        // 2, 3: row g + 8. The reference moves only when an exponent passes kSlack (fp16 holds weights up to 2^15), so
-        // that most steps neither reduce over the row's lanes nor touch the accumulators.
+        // 2, 3: row g + 8. The reference moves only when an exponent passes kSlack, so that most steps neither reduce over
+        // the row's lanes nor touch the accumulators.
         auto sees = [&](int j, int i) {
             const int t = 8 * j + token_of(2 * c + (i & 1));
             return ((tok >> t) & 1u) && t0 + t <= hi[i >> 1] && t0 + t >= lo[i >> 1];
@@ -293,9 +306,8 @@ struct Worker {
         for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
         // the accumulators' factors: of the references, and of V's unit
         float f[2] = {1.f, 1.f};
-#pragma unroll
-        for (int b = 0; b < HV; ++b) floor = fmaxf(floor, vs[b] * 0x1p-64f);
-        const bool far = vs[0] < floor || vs[HV - 1] < floor;
+        const float floor1 = HV == 1 ? floor : fmaxf(floor, vs[0] * 0x1p-64f);       // of the step's second half
+        const bool far = vs[0] < floor || vs[HV - 1] < floor1;
         const bool move = __any_sync(0xffffffffu, top > kSlack || none[0] || none[1] || far);
         if (move) {
 #pragma unroll
@@ -305,18 +317,20 @@ struct Worker {
                 for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[j][2 * r], x[j][2 * r + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (mx > (none[r] ? kNegInf : 0.f)) {
-                    f[r] = none[r] ? 0.f : ex2(-mx);
-                    m[r] = none[r] ? mx : m[r] + mx;
+                if (mx > (none[r] ? kNegInf : kBias)) {
+                    const float by = mx - kBias;
+                    f[r] = none[r] ? 0.f : ex2(-by);
+                    m[r] = none[r] ? by : m[r] + by;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) { x[j][2 * r] -= mx; x[j][2 * r + 1] -= mx; }
+                    for (int j = 0; j < 4; ++j) { x[j][2 * r] -= by; x[j][2 * r + 1] -= by; }
                 }
                 l[r] *= f[r];
             }
             if (far) {      // rare: weights smaller by what the unit does not hold, but whole in the rows' sums
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float s = vs[HV == 1 ? 0 : j >> 1], lack = s < floor ? log2f(s) - log2f(floor) : 0.f;
+                    const float s = vs[HV == 1 ? 0 : j >> 1], fl = j < 2 ? floor : floor1;
+                    const float lack = s < fl ? log2f(s) - log2f(fl) : 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         l[i >> 1] += ex2(x[j][i]) - ex2(x[j][i] + lack);
@@ -336,55 +350,61 @@ struct Worker {
                 x[j][i] = ex2(x[j][i]);
                 l[i >> 1] += x[j][i];
             }
+        // P V for NH halves at a time, 16 tokens each. An fp32 output takes both where they have one V scale: the tensor
+        // core's own running sum truncates, so each such sum starts anew and is added in fp32.
+        constexpr int NH = PSPLIT && HV == 1 ? 2 : 1, W = D / 32;      // W: words a lane takes of a row
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {       // 16 tokens of one V scale
+        for (int h0 = 0; h0 < 2; h0 += NH) {
             if constexpr (HV == 2) {
-                if (hf == 1 && vs[1] != vu) {
+                if (h0 == 1 && vs[1] != vu) {
                     const float u = enter(vs[1]);
                     scale_o(u, u);
                 }
             }
-            uint32_t p[4], pl[4];
-            float(&xa)[4] = x[2 * hf], (&xb)[4] = x[2 * hf + 1];
-            if constexpr (PSPLIT) {
-                split_h2(xa[0], xa[1], p[0], pl[0]);
-                split_h2(xa[2], xa[3], p[1], pl[1]);
-                split_h2(xb[0], xb[1], p[2], pl[2]);
-                split_h2(xb[2], xb[3], p[3], pl[3]);
-            } else {
-                p[0] = pack_h2(xa[0], xa[1]); p[1] = pack_h2(xa[2], xa[3]);
-                p[2] = pack_h2(xb[0], xb[1]); p[3] = pack_h2(xb[2], xb[3]);
-            }
-            // this lane's four V rows of the half: k = 2c, 2c + 1, 2c + 8, 2c + 9
-            const int ra = 16 * hf + token_of(2 * c), rb = 16 * hf + token_of(2 * c + 1);
-            constexpr int W = D / 32;           // words a lane takes of a row
-            uint32_t v[4][W];
+            uint32_t p[NH][4], pl[NH][4], v[NH][4][W];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = (i & 1 ? rb : ra) + (i >> 1) * 8;
-                if constexpr (D == 128) {
-                    const int ch = (g & 1) * 4 + (g >> 1);
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                                 : "r"(sv + r * D + ((ch ^ (r & 7)) << 4)));
+            for (int k = 0; k < NH; ++k) {
+                const int hf = h0 + k;
+                float(&xa)[4] = x[2 * hf], (&xb)[4] = x[2 * hf + 1];
+                if constexpr (PSPLIT) {
+                    split_weight(xa[0], xa[1], p[k][0], pl[k][0]);
+                    split_weight(xa[2], xa[3], p[k][1], pl[k][1]);
+                    split_weight(xb[0], xb[1], p[k][2], pl[k][2]);
+                    split_weight(xb[2], xb[3], p[k][3], pl[k][3]);
                 } else {
-                    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                                 : "=r"(v[i][0]), "=r"(v[i][1])
-                                 : "r"(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
+                    p[k][0] = pack_h2(xa[0], xa[1]); p[k][1] = pack_h2(xa[2], xa[3]);
+                    p[k][2] = pack_h2(xb[0], xb[1]); p[k][3] = pack_h2(xb[2], xb[3]);
                 }
-            }
-            if (edge) {
-                // Rows that do not exist hold anything, and 0 * NaN would reach rows that do not see the NaN: both are taken
-                // out, and a NaN is noted (the rows it belongs to are found when the unit is done).
+                // this lane's four V rows of the half: k = 2c, 2c + 1, 2c + 8, 2c + 9
+                const int ra = 16 * hf + token_of(2 * c), rb = 16 * hf + token_of(2 * c + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = (i & 1 ? rb : ra) + (i >> 1) * 8;
-                    const uint32_t keep = (tok >> r) & 1u ? 0xffffffffu : 0u;
+                    uint32_t(&vr)[W] = v[k][i];
+                    if constexpr (D == 128) {
+                        const int ch = (g & 1) * 4 + (g >> 1);
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(vr[0]), "=r"(vr[1]), "=r"(vr[2]), "=r"(vr[3])
+                                     : "r"(sv + r * D + ((ch ^ (r & 7)) << 4)));
+                    } else {
+                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                                     : "=r"(vr[0]), "=r"(vr[1])
+                                     : "r"(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
+                    }
+                }
+                if (edge) {
+                    // Rows that do not exist hold anything, and 0 * NaN would reach rows that do not see the NaN: both are
+                    // taken out, and a NaN is noted (the rows it belongs to are found when the unit is done).
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const uint32_t isnan = __vcmpeq4(v[i][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) & keep;
-                        saw_nan |= isnan != 0u;
-                        v[i][w] &= keep & ~isnan;
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (i & 1 ? rb : ra) + (i >> 1) * 8;
+                        const uint32_t keep = (tok >> r) & 1u ? 0xffffffffu : 0u;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            const uint32_t isnan = __vcmpeq4(v[k][i][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) & keep;
+                            saw_nan |= isnan != 0u;
+                            v[k][i][w] &= keep & ~isnan;
+                        }
                     }
                 }
             }
@@ -394,19 +414,22 @@ struct Worker {
                 for (int q = 0; q < 4; ++q) {
                     // column 4 w + q of the lane's chunk: the two rows' bytes side by side, then as fp16 pair
                     const uint32_t sel = q | ((4 + q) << 4);
-                    const uint32_t b0 = e4m3x2_to_h2(__byte_perm(v[0][w], v[1][w], sel));
-                    const uint32_t b1 = e4m3x2_to_h2(__byte_perm(v[2][w], v[3][w], sel));
                     float(&acc)[4] = o[4 * w + q];
-                    if constexpr (PSPLIT) {
-                        // an fp32 output: the tensor core's own running sum truncates, so each half's sum starts anew
-                        // and is added in fp32
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma16816(t, pl, b0, b1);
-                        mma16816(t, p, b0, b1);
+                    float t[4] = {0.f, 0.f, 0.f, 0.f}, tl[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[r] += t[r];
-                    } else {
-                        mma16816(acc, p, b0, b1);
+                    for (int k = 0; k < NH; ++k) {
+                        const uint32_t b0 = e4m3x2_to_h2(__byte_perm(v[k][0][w], v[k][1][w], sel));
+                        const uint32_t b1 = e4m3x2_to_h2(__byte_perm(v[k][2][w], v[k][3][w], sel));
+                        if constexpr (PSPLIT) {
+                            mma16816(tl, pl[k], b0, b1);
+                            mma16816(t, p[k], b0, b1);
+                        } else {
+                            mma16816(acc, p[k], b0, b1);
+                        }
+                    }
+                    if constexpr (PSPLIT) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[r] += fmaf(tl[r], 1.f / kLowPart, t[r]);
                     }
                 }
         }
@@ -623,14 +646,16 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             if (ok && x.tok != 0u) w.step(sk, sk + S::kStepBytes, x.t, x.ks, x.vs, x.tok, x.edge);
         }
 
-        // ---- the four warps' parts of each row
+        // ---- the four warps' parts of each row, against references kSlack higher: weights up to 1, so that the sums of
+        // weights times values are finite wherever the tokens' number times the largest value is
+        const float out_unit = w.vu * kDown;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
             w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 2);
             if (c == 0) {
-                s_ml[warp][g + 8 * r][0] = w.m[r];
-                s_ml[warp][g + 8 * r][1] = w.l[r];
+                s_ml[warp][g + 8 * r][0] = w.m[r] + kSlack;
+                s_ml[warp][g + 8 * r][1] = w.l[r] * kDown;
             }
         }
         const bool nans = __syncthreads_or(w.saw_nan);      // (and every warp is through its ring)
@@ -643,11 +668,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             const int x0 = 16 * c, x1 = D == 128 ? 64 + 16 * c : 16 * c + 8;
 #pragma unroll
             for (int i = 0; i < W::NT; i += 4) {
-                *reinterpret_cast<float4 *>(row + x0 + i) = make_float4(w.o[i][2 * r] * w.vu, w.o[i + 1][2 * r] * w.vu,
-                                                                        w.o[i + 2][2 * r] * w.vu, w.o[i + 3][2 * r] * w.vu);
+                *reinterpret_cast<float4 *>(row + x0 + i) = make_float4(w.o[i][2 * r] * out_unit, w.o[i + 1][2 * r] * out_unit,
+                                                                        w.o[i + 2][2 * r] * out_unit, w.o[i + 3][2 * r] * out_unit);
                 *reinterpret_cast<float4 *>(row + x1 + i) =
-                    make_float4(w.o[i][2 * r + 1] * w.vu, w.o[i + 1][2 * r + 1] * w.vu, w.o[i + 2][2 * r + 1] * w.vu,
-                                w.o[i + 3][2 * r + 1] * w.vu);
+                    make_float4(w.o[i][2 * r + 1] * out_unit, w.o[i + 1][2 * r + 1] * out_unit, w.o[i + 2][2 * r + 1] * out_unit,
+                                w.o[i + 3][2 * r + 1] * out_unit);
             }
         }
         __syncthreads();

@@ -461,17 +461,19 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  workspace    device memory of at least gdn_kv_attn_workspace_bytes(...) bytes, 16-byte
  *               aligned, owned by the caller; contents irrelevant on entry and unspecified on
  *               return. Calls that may overlap on the GPU need one each.
- *  Sums and softmax statistics are fp32. Queries are scaled by a power of two for each row and
- *  enter the products as two fp16 parts (fp32 queries: 22 bits), as fp16 (bf16 queries, fp32
- *  output: exact) or, with a bf16 output, as two e4m3 parts (bf16 queries: exact down to 2^-9
- *  of the row's largest element, within 2^-17.8 of that element below). The weights enter as
- *  fp16 with a bf16 output, and as two fp16 parts with an fp32 one. V scales of a request's
- *  blocks may be any powers of two apart; from 2^64 below the largest on, a block's values
- *  enter with what is missing in their weights (lost where those fall below fp16's 2^-25). A
- *  position that a query
- *  does not see does not reach its result, whatever its values; a NaN that it sees (append
- *  stores infinities as NaN) makes its result NaN, a NaN of V in that column alone. Infinite
- *  queries give NaN.
+ *  Sums and softmax statistics are fp32; results are finite while the number of tokens times
+ *  the largest |value| is within fp32. Queries are scaled by a power of two for each row and
+ *  enter the products as two fp16 parts (fp32 queries) or one (bf16 queries, fp32 output): both
+ *  within 2^-25 of the row's largest element, the latter exact down to 2^-17 of it; with a bf16
+ *  output and bf16 queries as two e4m3 parts (exact down to 2^-9 of the row's largest element,
+ *  within 2^-17.8 of that element below). The weights enter as two fp16 parts with an fp32
+ *  output (within 2^-23 of themselves or 2^-44 of the row's largest weight), and as one with a
+ *  bf16 output (within 2^-12 of themselves or 2^-32 of the largest; 2^-25 in the many-rows
+ *  kernel). V scales of a request's blocks may be any powers of two apart; from 2^64 below the
+ *  largest on, a block's weights carry what is missing (and are lost below those bounds). A
+ *  position that a query does not see does not reach its result, whatever its values; a NaN
+ *  that it sees (append stores infinities as NaN) makes its result NaN, a NaN of V in that
+ *  column alone. Infinite queries give NaN.
  *  Requests of more than 64 rows (query tokens x query heads of a KV head) run on a tcgen05
  *  kernel when q and o are bf16 and the batch may hold prompts of thousands of rows: (T - N + 1)
  *  * Hq of 40 (d = 128) or 58 (d = 64) rows for each SM, max_q_len * Hq / Hkv above 64. All

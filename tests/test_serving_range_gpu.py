@@ -245,3 +245,36 @@ def test_attn_of_a_query_that_is_not_finite_is_nan(S, lib, dtype, out, pad, sign
     assert torch.equal(torch.isnan(o[:n]).all(-1).cpu(), want) and torch.equal(torch.isnan(o[:n]).any(-1).cpu(), want)
     assert torch.equal(torch.isnan(lse[:n]).cpu(), want)
     assert (o[71:74] == 0).all() and (lse[71:74] == -math.inf).all()
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("nats", [10, 20, 25])
+@pytest.mark.parametrize("d,bs,dtype", [(128, 64, torch.bfloat16), (64, 16, torch.float32), (64, 32, torch.bfloat16)])
+@pytest.mark.parametrize("n", [600, 6000])
+def test_attn_fp32_output_keeps_small_weights(S, lib, n, d, bs, dtype, nats):
+    """One token `nats` above thousands of others, itself with a V of zeros: the others' weights, down to 2^-36 of
+    the largest, carry the whole result. Two fp16 parts, the second 2^12 larger, of weights that start at 2^7: the
+    smallest half step is 2^-25 2^-12 2^-7 = 2^-44 of the largest weight for each token, beside the tolerance of
+    the other fp32 outputs."""
+    cache, q, table, tab, cu = attn_case(S, [n], [1], 2, 4, d, bs, dtype, seed=60)
+    g = _gen(61)
+    q.copy_(torch.where(torch.randn(1, 2, 1, d, generator=g, device=DEV) > 0, 1.0, -1.0).expand(1, 2, 4, d).reshape(1, 8, d))
+    k = torch.randn(cache.k.shape, generator=g, device=DEV)
+    at = 37                                               # the token above the others: its key lies along the queries
+    b, r = table[0][at // bs], at % bs
+    k[b, :, r] = 16.0 * q[0, ::4].float()
+    cache.k.copy_(k.to(cache.k.dtype))
+    cache.k_scale.fill_(1.0)
+    v = cache.v.float().abs().clamp(min=1.0)
+    v[b, :, r] = 0.0
+    cache.v.copy_(v.to(cache.v.dtype))
+    cache.v_scale.fill_(2.0 ** -8)
+    scale = nats / (16.0 * d)
+    o, lse = S.gdn_kv_attn(cache, q, tab, i32(cu), i32([n]), scale=scale, lse=True)
+    assert lib.gdn_sync_status() == 0
+    ro, rl, A, ds, vm = attn_ref(cache, q, table, cu, [n], 0, scale)
+    tol = 2.0 ** -24 * ro.abs() + A * (2 * ds[..., None] + 2.0 ** -21 + 2.0 ** -22 + min(n * 2.0 ** -23, 2.0 ** -11))
+    tol = tol + n * 2.0 ** -44 * vm[..., None]
+    err = (o.double().cpu() - ro).abs()
+    assert (err <= tol).all(), (err / tol).max()
+    assert ((lse.double().cpu() - rl).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()
