@@ -187,9 +187,21 @@ def gdn_kv_append(cache: KvCache, k, v, slot_map, stream=None) -> KvCache:
 
 
 @functools.lru_cache(maxsize=1024)
-def gdn_kv_attn_workspace_bytes(N: int, T: int, Hq: int, Hkv: int, d: int, max_q_len: int = 1) -> int:
-    """Bytes of device workspace gdn_kv_attn needs (0 for unsupported sizes)."""
-    return int(lib.gdn_kv_attn_workspace_bytes(N, T, Hq, Hkv, d, max_q_len))
+def _workspace_bytes(index: Optional[int], N: int, T: int, Hq: int, Hkv: int, d: int, max_q_len: int) -> int:
+    """The size on device ``index`` (it grows with the device's SMs); None: no device."""
+    if index is None or index == _device_now():
+        return int(lib.gdn_kv_attn_workspace_bytes(N, T, Hq, Hkv, d, max_q_len))
+    with torch.cuda.device(index):
+        return int(lib.gdn_kv_attn_workspace_bytes(N, T, Hq, Hkv, d, max_q_len))
+
+
+def gdn_kv_attn_workspace_bytes(N: int, T: int, Hq: int, Hkv: int, d: int, max_q_len: int = 1, device=None) -> int:
+    """Bytes of device workspace gdn_kv_attn needs on ``device`` (the current one when None; 0 for unsupported sizes)."""
+    index = None
+    if torch.cuda.is_available():
+        index = torch.device("cuda" if device is None else device).index
+        index = _device_now() if index is None else index
+    return _workspace_bytes(index, N, T, Hq, Hkv, d, max_q_len)
 
 
 def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: int = 1, window: int = 0,
@@ -222,7 +234,7 @@ def gdn_kv_attn(cache: KvCache, q, block_table, cu_seqlens, kv_lens, max_q_len: 
         raise TypeError(f"o / out_dtype must be float32 or bfloat16, got {odt}")
     dt = _lib._dtype_code(q)
     raw = _stream_of(dev, stream)
-    need = gdn_kv_attn_workspace_bytes(N, T, Hq, cache.heads, d, max_q_len)
+    need = _workspace_bytes(dev.index, N, T, Hq, cache.heads, d, max_q_len)
     if o is None:
         o = _new(q, (T, Hq, d), odt, stream)
     else:

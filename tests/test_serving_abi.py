@@ -158,3 +158,45 @@ def test_binding_refuses():
         S.gdn_decode_slots(k, k, torch.zeros(5, 3, 64), None, None, torch.zeros(4, 3, 64, 64), i(5))
     with pytest.raises(ValueError):                  # state of other sizes
         S.gdn_decode_slots(k, k, k, None, None, torch.zeros(4, 2, 64, 128), i(5))
+
+
+def test_workspace_size_is_each_device_s_own(monkeypatch):
+    """The size goes by the SMs of the device that the call runs on, so one device's is not another's."""
+    from gated_deltanet_sequence_b200 import serving as S
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.back, now[0] = now[0], self.index
+
+        def __exit__(self, *a):
+            now[0] = self.back
+
+    class Lib:
+        calls = 0
+
+        @staticmethod
+        def gdn_kv_attn_workspace_bytes(N, T, Hq, Hkv, d, max_q_len):
+            Lib.calls += 1
+            return 1000 * (1 + now[0]) + N
+
+    monkeypatch.setattr(S, "lib", Lib)
+    monkeypatch.setattr(S, "_device_now", lambda: now[0])
+    monkeypatch.setattr(S.torch.cuda, "device", Device)
+    monkeypatch.setattr(S.torch.cuda, "is_available", lambda: True)
+    S._workspace_bytes.cache_clear()
+    try:
+        size = S.gdn_kv_attn_workspace_bytes
+        for _ in range(2):
+            assert size(3, 3, 8, 2, 128) == 1003 and size(3, 3, 8, 2, 128, device="cuda:1") == 2003
+            assert size(3, 3, 8, 2, 128, device="cuda") == 1003 and now == [0]
+            now[0] = 2
+            assert size(3, 3, 8, 2, 128) == 3003 and size(3, 3, 8, 2, 128, device=torch.device("cuda", 0)) == 1003
+            assert now == [2]
+            now[0] = 0
+        assert Lib.calls == 3
+    finally:
+        S._workspace_bytes.cache_clear()
