@@ -504,7 +504,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         const int p_first = rw.kv - rw.qlen + rt * kRows / G;
         const int p_last = rw.kv - rw.qlen + min(rt * kRows + kRows - 1, rows - 1) / G;
         // tokens of this part that some row sees
-        const int t_lo = max((rw.tile0 + tile0) * kTile, a.window > 0 ? max(0, p_first - a.window + 1) / kTile * kTile : 0);
+        const int t_lo = max((rw.tile0 + tile0) * kTile, a.window > 0 ? max(0, max(p_first, -1) - a.window + 1) / kTile * kTile : 0);
         const int t_hi = min((rw.tile0 + tile0 + ntile) * kTile, p_last + 1);
 
         W w;
@@ -571,7 +571,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
                 for (int i = 0; i < 4; ++i) load4(in ? qp + 16 * (c + 4 * half) + 4 * i : nullptr, &qf[r][16 * half + 4 * i]);
             w.hi[r] = in ? rw.kv - rw.qlen + tok : -1;
-            w.lo[r] = a.window > 0 ? w.hi[r] - a.window + 1 : 0;
+            w.lo[r] = a.window > 0 ? max(w.hi[r], -1) - a.window + 1 : 0;      // (rows before position 0 see nothing anyway)
             w.m[r] = kNegInf;
             w.l[r] = 0.f;
         }
@@ -591,7 +591,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         w.floor = 0x1p-100f;
         w.saw_nan = false;
 
-        const int lo_last = a.window > 0 ? p_last - a.window + 1 : 0;
+        const int lo_last = a.window > 0 ? max(p_last, -1) - a.window + 1 : 0;
         bool ok = true;
         struct Step {
             int t;
@@ -703,7 +703,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             const int R = rt * kRows + r;
             if (nans) {        // rare: the row's own positions are looked through for NaN in these columns
-                const int pos = rw.kv - rw.qlen + R / G, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                const int pos = rw.kv - rw.qlen + R / G, lo = a.window > 0 ? max(0, max(pos, -1) - a.window + 1) : 0;
                 for (int t = max(t_lo, lo); t < min(t_hi, pos + 1); ++t) {
                     const int id = table[t >> a.bs_log2];
                     if (id < 0 || id >= a.num_blocks) continue;

@@ -290,7 +290,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         pf[g] = p0 + r0 / G;
         pl[g] = r1 >= r0 ? p0 + r1 / G : -1;
         tb[g] = pl[g] >= 0 ? pl[g] / kTok + 1 : 0;
-        ta[g] = a.window > 0 ? min(tb[g], max(0, pf[g] - a.window + 1) / kTok) : 0;
+        ta[g] = a.window > 0 ? min(tb[g], max(0, max(pf[g], -1) - a.window + 1) / kTok) : 0;
     }
     if (tb[1] == 0) ta[1] = tb[1] = tb[0];               // no rows: after the other's tiles
     if (tb[0] == 0) ta[0] = tb[0] = ta[1];
@@ -566,8 +566,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_Q]);
         }
-        const int hi = in ? p0 + tok : -1, lo = a.window > 0 ? hi - a.window + 1 : 0;
-        const int lo_last = a.window > 0 ? pl[g] - a.window + 1 : 0;
+        const int hi = in ? p0 + tok : -1, lo = a.window > 0 ? max(hi, -1) - a.window + 1 : 0;
+        const int lo_last = a.window > 0 ? max(pl[g], -1) - a.window + 1 : 0;
         float m = kNegInf, l = 0.f;
         int done = 0;                                    // tiles of this group so far
         bool ok = true;

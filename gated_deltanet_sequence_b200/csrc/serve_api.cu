@@ -29,6 +29,8 @@ long long esize(gdn_dtype_t t) { return t == GDN_BF16 ? 2 : 4; }
 bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 bool head_ok(int d) { return d == 64 || d == 128; }
 constexpr long long kMaxRows = 1ll << 30, kInt = 2147483647ll;
+// Positions of gdn_kv_attn: its kernels look a few thousand positions past a context's end in 32 bits.
+constexpr long long kMaxContext = kInt - 65535;
 // rows of `width` elements, `stride` apart, T of them: 16-byte vectors stay aligned and offsets fit
 bool stride_ok(long long stride, long long width, gdn_dtype_t t) {
     return stride >= width && stride <= (1ll << 40) && (stride * esize(t)) % 16 == 0;
@@ -85,7 +87,7 @@ gdn_status_t gdn_kv_attn(const void *q, long long q_stride, const void *k_cache,
         return GDN_ERR_INVALID_ARG;
     if (!head_ok(d) || !block_size_ok(block_size) || Hq > 65535 || T > kMaxRows) return GDN_ERR_UNSUPPORTED;
     if (static_cast<long long>(num_blocks) * Hkv * block_size > kInt ||
-        static_cast<long long>(max_blocks) * block_size > kInt)
+        static_cast<long long>(max_blocks) * block_size > kMaxContext)
         return GDN_ERR_INVALID_ARG;
     if (!al(k_cache, 16) || !al(v_cache, 16) || !al(k_scale, 4) || !al(v_scale, 4) || !al(block_table, 4) ||
         !al(cu_seqlens, 4) || !al(kv_lens, 4) || !al_opt(lse, 4) || !al(workspace, 16) ||

@@ -480,8 +480,8 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  others run on the kernel for few rows, which reads the cache once for each 16 rows. Both hold
  *  the bounds above.
  *  N >= 1, T >= 0, 1 <= Hkv <= Hq, Hq % Hkv == 0, Hq <= 65535, d in {64, 128}, block_size in
- *  {16, 32, 64, 128}, window >= 0, scale finite; num_blocks * Hkv * block_size and max_blocks *
- *  block_size < 2^31; q, o, caches 16-byte aligned, the row stride of q a multiple of 16 bytes.
+ *  {16, 32, 64, 128}, window >= 0, scale finite; num_blocks * Hkv * block_size < 2^31,
+ *  max_blocks * block_size <= 2^31 - 2^16; q, o, caches 16-byte aligned, the row stride of q a multiple of 16 bytes.
  */
 size_t gdn_kv_attn_workspace_bytes(int N, int T, int Hq, int Hkv, int d, int max_q_len);
 gdn_status_t gdn_kv_attn(const void *q, long long q_stride, const void *k_cache, const void *v_cache,

@@ -74,6 +74,13 @@ def test_attn_rejects_bad_arguments(lib, kw, want):
     assert _attn(lib, **kw) == want
 
 
+def test_attn_rejects_tables_whose_positions_pass_32_bits(lib):
+    """The kernels look a few thousand positions past a context's end: max_blocks * block_size <= 2^31 - 2^16."""
+    for bs in (16, 128):
+        most = (2 ** 31 - 2 ** 16) // bs
+        assert _attn(lib, mb=most, bs=bs, T=0) == 0 and _attn(lib, mb=most + 1, bs=bs, T=0) == 1
+
+
 def test_attn_workspace_size(lib):
     size = lib.lib.gdn_kv_attn_workspace_bytes
     assert size(1, 1, 8, 2, 128, 1) > 0 and size(1, 1, 8, 2, 128, 1) % 16 == 0

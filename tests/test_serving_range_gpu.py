@@ -278,3 +278,38 @@ def test_attn_fp32_output_keeps_small_weights(S, lib, n, d, bs, dtype, nats):
     err = (o.double().cpu() - ro).abs()
     assert (err <= tol).all(), (err / tol).max()
     assert ((lse.double().cpu() - rl).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()
+
+
+# ---------------------------------------------------------------- positions at the ends of their range
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_attn_windows_near_2_to_31(S, lib, out):
+    """The widest window that a table still outgrows, and 70000 rows of which all but three lie before position 0."""
+    n, kv, d, bs = 70000, 3, 64, 16
+    cache, q, table, tab, cu = attn_case(S, [kv], [n], 1, 1, d, bs, torch.bfloat16, seed=70)
+    wide = torch.full((1, (2 ** 31 - 2 ** 16) // bs), -1, dtype=torch.int32, device=DEV)
+    wide[:, :tab.shape[1]] = tab
+    kw = dict(max_q_len=n, scale=0.125, out_dtype=out, lse=True)
+    want = S.gdn_kv_attn(cache, q, wide, i32(cu), i32([kv]), **kw)
+    got = S.gdn_kv_attn(cache, q, wide, i32(cu), i32([kv]), window=2 ** 31 - 2 ** 16 - 1, **kw)
+    assert lib.gdn_sync_status() == 0
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    o, lse = got
+    assert (o[:-kv] == 0).all() and (lse[:-kv] == -math.inf).all() and torch.isfinite(lse[-kv:]).all()
+    one = S.gdn_kv_attn(cache, q[-kv:], tab, i32([0, kv]), i32([kv]), max_q_len=kv, scale=0.125, lse=True)
+    assert (o[-kv:].float() - one[0]).abs().max() <= 2.0 ** -7 * one[0].abs().max()
+    assert (lse[-kv:] - one[1]).abs().max() <= 2.0 ** -18
+
+
+def test_attn_over_the_longest_context(S, lib):
+    """2^31 - 2^16 tokens, one block of 128 named throughout: the result of that block alone, its lse with log n more.
+    Each of a warp's 57000 steps adds a rounding of 2^-24 to sums that it carries: 2^-8 at the worst."""
+    n, d, bs = 2 ** 31 - 2 ** 16, 64, 128
+    cache, q, table, tab, cu = attn_case(S, [bs], [1], 1, 8, d, bs, torch.bfloat16, seed=71)
+    long = torch.full((1, n // bs), table[0][0], dtype=torch.int32, device=DEV)
+    one = S.gdn_kv_attn(cache, q, tab, i32(cu), i32([bs]), scale=0.125, lse=True)
+    for window in (0, n - 1):
+        o, lse = S.gdn_kv_attn(cache, q, long, i32(cu), i32([n]), scale=0.125, window=window, lse=True)
+        assert lib.gdn_sync_status() == 0
+        assert (o - one[0]).abs().max() <= 2.0 ** -7 * one[0].abs().max()
+        assert (lse - one[1] - math.log(n // bs)).abs().max() <= 2.0 ** -7
