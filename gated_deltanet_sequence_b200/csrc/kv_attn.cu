@@ -465,6 +465,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
     const uint32_t ring = smem_u32(smem) + warp * S::kRing;
     uint32_t phase = 0;                     // parity bit of each stage
+    uint32_t live = 0;                      // stages with copies in flight
+    bool ok = true;                         // this warp's copies arrive
     constexpr int br = kStep / HV;          // rows of a TMA box
 
     int n = sh.n;
@@ -577,9 +579,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         }
         fetch_blocks(cur, 0);
         nxt = cur;
-        uint32_t live = 0;                  // steps in flight that have copies, by stage
         for (int i = 0; i < min(nstep, S::kStages - 1); ++i)
-            if (issue(i, i, cur)) live |= 1u << i;
+            if (ok && issue(i, i, cur)) live |= 1u << i;
 
         const int nrows = min(kRows, rows - rt * kRows);        // rows of this tile
         w.set_query(0, qf[0], a.scale_log2);
@@ -592,7 +593,6 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         w.saw_nan = false;
 
         const int lo_last = a.window > 0 ? max(p_last, -1) - a.window + 1 : 0;
-        bool ok = true;
         struct Step {
             int t;
             float ks[HV], vs[HV];
@@ -620,10 +620,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         auto turn = [&](int i) {            // sends a later step's copies out, waits for this one's
             __syncwarp();
             const int nx = i + S::kStages - 1;
-            if (nx < nstep && ok) {
-                const uint32_t bit = 1u << nst;
-                live = issue(nx, nst, (nx >> 5) == (i >> 5) ? cur : nxt) ? live | bit : live & ~bit;
-            }
+            if (nx < nstep && ok && issue(nx, nst, (nx >> 5) == (i >> 5) ? cur : nxt)) live |= 1u << nst;
             if (ok && (live & (1u << st))) {
                 const uint32_t par = (phase >> st) & 1u;
                 if (!bounded_wait(&s_bar[warp][st], par, a.wait_limit)) {
@@ -634,6 +631,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 phase ^= 1u << st;
+                live ^= 1u << st;
             }
             const uint32_t sk = ring + st * S::kStageBytes;
             nst = st;
@@ -644,6 +642,13 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             const Step x = look(i);
             const uint32_t sk = turn(i);
             if (ok && x.tok != 0u) w.step(sk, sk + S::kStepBytes, x.t, x.ks, x.vs, x.tok, x.edge);
+        }
+        // A copy that did not come even within the drain's limit: the others in flight are waited for as well, before their
+        // buffers are used for the merge or the block ends, and this warp sends no more.
+        if (!ok) {
+            for (int i = 0; i < S::kStages; ++i)
+                if (live & (1u << i)) bounded_wait(&s_bar[warp][i], (phase >> i) & 1u, kDrainLimitCycles);
+            live = 0;
         }
 
         // ---- the four warps' parts of each row, against references kSlack higher: weights up to 1, so that the sums of
