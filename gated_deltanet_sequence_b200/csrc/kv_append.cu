@@ -277,7 +277,8 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
         for (int j = 0; j < STEPS; ++j)
             if (tid / CPR + j * (kAppThreads / CPR) < len)
                 store_codes(cache, blk0 + off * D + (tid + j * kAppThreads) * 8, ncodes, c[j], inv, odd, err);
-        if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, tid, kAppThreads);
+        if (off > 0 && sc != old && in_bounds(blk0 + off * D - 1, ncodes, err))
+            rescale_codes(cache + blk0, off * D, old * inv, tid, kAppThreads);
         // everyone has read the old scale: each did before the barrier above
         if (tid == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     };
@@ -327,7 +328,8 @@ kv_append_kernel(const AppArgs a, unsigned *__restrict__ err) {
             const int id = lane + j * 32;
             if (id < len * CPR) store_codes(cache, blk0 + off * D + id * 8, ncodes, w[j], inv, odd, err);
         }
-        if (off > 0 && sc != old) rescale_codes(cache + blk0, off * D, old * inv, lane, 32);
+        if (off > 0 && sc != old && in_bounds(blk0 + off * D - 1, ncodes, err))
+            rescale_codes(cache + blk0, off * D, old * inv, lane, 32);
         __syncwarp();
         if (lane == 0 && (off == 0 || sc != old)) scale[bh] = sc;
     }

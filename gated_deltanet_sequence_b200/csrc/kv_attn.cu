@@ -523,7 +523,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 bank.blk[b] = -1;
                 bank.ksc[b] = bank.vsc[b] = 1.f;
                 if (t < t_hi) {
-                    const int id = table[t >> a.bs_log2];
+                    const int id = in_bounds(t >> a.bs_log2, a.max_blocks, a.err) ? table[t >> a.bs_log2] : -1;
                     if (id >= 0 && id < a.num_blocks) {
                         bank.blk[b] = id;
                         bank.ksc[b] = a.k_scale[static_cast<long long>(id) * a.Hkv + h];

@@ -326,7 +326,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const int bl = a.bs >> 4;                        // 16-token groups of a block
         auto look = [&](int j) {                         // block of this lane's 16-token group of tile j
             const int t = (t_a + j) * kTok + 16 * lane;
-            const int id = lane < 8 && j < nt && t < t_hi ? table[t >> a.bs_log2] : -1;
+            const int id = lane < 8 && j < nt && t < t_hi && in_bounds(t >> a.bs_log2, a.max_blocks, a.err) ? table[t >> a.bs_log2] : -1;
             return id < a.num_blocks ? id : -1;
         };
         int id_next = look(0), last = -1;
@@ -425,7 +425,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // that an instruction of the same tile waited for would hold up the conversion (1300 cycles a tile).
         auto block_of = [&](int j) {
             const int t = (t_a + j) * kTok + tk;
-            return j < nt && t < t_hi ? table[t >> a.bs_log2] : -1;
+            return j < nt && t < t_hi && in_bounds(t >> a.bs_log2, a.max_blocks, a.err) ? table[t >> a.bs_log2] : -1;
         };
         auto scale_of = [&](int id) {
             return id >= 0 && id < a.num_blocks ? a.v_scale[static_cast<long long>(id) * a.Hkv + h] : -1.f;

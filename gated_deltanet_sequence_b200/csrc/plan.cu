@@ -67,7 +67,8 @@ __device__ __forceinline__ void plan_token(const PlanArgs &a, const int *cu, int
     if (t < total) {
         n = find_range(cu, a.N, t);
         p = a.kv[n] - (cu[n + 1] - t);
-        const int b = a.table[static_cast<long long>(n) * a.max_blocks + (p >> a.bs_log2)];
+        const long long at = static_cast<long long>(n) * a.max_blocks + (p >> a.bs_log2);
+        const int b = in_bounds(at, static_cast<long long>(a.N) * a.max_blocks, err) ? a.table[at] : -1;
         if (b >= 0 && b < a.num_blocks) slot = (b << a.bs_log2) + (p & ((1 << a.bs_log2) - 1));
         else if (b >= a.num_blocks || !may_be_short) atomicOr(err, kErrBadSeqlens);
     }
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
 
     // ---- finished requests' blocks go on top of the free list, in (request, block) order
     const long long rows = static_cast<long long>(ngone) * a.max_blocks;
+    const long long entry_count = static_cast<long long>(a.N) * a.max_blocks;      // (bounds checks of the debug build)
     for (long long base = 0; base < rows; base += 4 * kPlanThreads) {      // four entries a thread
         const long long i0 = base + 4 * tid;
         int b[4], have = 0;
@@ -161,7 +163,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
             b[k] = -1;
             if (i0 + k < rows) {
                 const int g = static_cast<int>((i0 + k) / a.max_blocks);
-                int *entry = a.table + static_cast<long long>(gone[g]) * a.max_blocks + (i0 + k - static_cast<long long>(g) * a.max_blocks);
+                const long long place = static_cast<long long>(gone[g]) * a.max_blocks + (i0 + k - static_cast<long long>(g) * a.max_blocks);
+                if (!in_bounds(place, entry_count, err)) continue;
+                int *entry = a.table + place;
                 b[k] = *entry;
                 if (b[k] != -1) *entry = -1;
                 if (b[k] < -1 || b[k] >= a.num_blocks) { atomicOr(err, kErrBadSeqlens); b[k] = -1; }
@@ -173,7 +177,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (b[k] >= 0) {
-                if (at < a.num_blocks) a.free_list[at] = b[k];
+                if (at < a.num_blocks) {
+                    if (in_bounds(at, a.num_blocks, err)) a.free_list[at] = b[k];
+                }
                 else atomicOr(err, kErrBadSeqlens);
                 ++at;
             }
@@ -185,7 +191,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
     auto new_entry = [&](int i) {
         const int n = find_range(blk, a.N, i);
         const int first = (a.kv[n] - (tok[n + 1] - tok[n]) + bs - 1) >> a.bs_log2;
-        return a.table + static_cast<long long>(n) * a.max_blocks + first + (i - blk[n]);
+        const long long place = static_cast<long long>(n) * a.max_blocks + first + (i - blk[n]);
+        return a.table + (in_bounds(place, entry_count, err) ? place : 0);
     };
     int want = 0, missing = 0;
     if (entries > kPlanThreads) {
@@ -204,7 +211,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, un
         const int r = block_prefix<int>(need ? 1 : 0, &sum);
         if (entries <= kPlanThreads) missing = max(0, sum - count);
         if (need && missing == 0) {
-            const int b = a.free_list[count - 1 - taken - r];
+            const int place = count - 1 - taken - r;
+            const int b = in_bounds(place, a.num_blocks, err) ? a.free_list[place] : -1;
             if (b >= 0 && b < a.num_blocks) *entry = b;
             else atomicOr(err, kErrBadSeqlens);
         }
