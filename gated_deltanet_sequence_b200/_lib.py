@@ -117,6 +117,26 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream, result: bool = True,
+         zero: bool = False) -> torch.Tensor:
+    """A tensor made on the stream that the call uses: what torch hands out on another one may be memory that work queued
+    there still reads or writes. A result made on a passed stream is read on the current one (by a caller who waits),
+    so it is kept until that is through with it too."""
+    make = like.new_zeros if zero else like.new_empty
+    if stream is None:
+        return make(shape, dtype=dtype)
+    dev = like.device
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)      # (0 is the default stream, which ExternalStream does not take)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype)
+    if result and here != stream:
+        t.record_stream(here)
+    return t
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return GDN_BF16
@@ -196,7 +216,7 @@ def lin_attn_chunk_fwd(q, k, v, g=None, o=None, s0=None, s_final=None, chunk: in
     _check("s0", s0, (B, H, dk, dv), torch.float32, dev, required=False)
     odt, opts = _out_opts(o, out_dtype, d_skip, H, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     if o is None:
-        o = torch.empty(B, H, L, dv, dtype=odt, device=dev)
+        o = _new(q, (B, H, L, dv), odt, stream)
     _check("o", o, (B, H, L, dv), odt, dev)
     _check("s_final", s_final, (B, H, dk, dv), torch.float32, dev, required=False)
     if opts is None:
@@ -228,7 +248,7 @@ def gdn_chunk_fwd(q, k, v, beta, g=None, o=None, s0=None, s_final=None, chunk: i
     _check("s0", s0, (B, H, dk, dv), torch.float32, dev, required=False)
     odt, opts = _out_opts(o, out_dtype, d_skip, H, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     if o is None:
-        o = torch.empty(B, H, L, dv, dtype=odt, device=dev)
+        o = _new(q, (B, H, L, dv), odt, stream)
     _check("o", o, (B, H, L, dv), odt, dev)
     _check("s_final", s_final, (B, H, dk, dv), torch.float32, dev, required=False)
     if opts is None:
@@ -275,7 +295,7 @@ def lin_attn_chunk_fwd_varlen(q, k, v, cu_seqlens, g=None, o=None, s0=None, s_fi
     vec = _check_gate(g, (H, T), dk, dev)
     odt, opts = _out_opts(o, out_dtype, d_skip, H, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     if o is None:
-        o = torch.zeros(H, T, dv, dtype=odt, device=dev)
+        o = _new(q, (H, T, dv), odt, stream, zero=True)
     _check("o", o, (H, T, dv), odt, dev)
     if opts is None:
         st = lib.lin_attn_chunk_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(o), _ptr(s0),
@@ -300,7 +320,7 @@ def gdn_chunk_fwd_varlen(q, k, v, beta, cu_seqlens, g=None, o=None, s0=None, s_f
     vec = _check_gate(g, (H, T), dk, dev)
     odt, opts = _out_opts(o, out_dtype, d_skip, H, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     if o is None:
-        o = torch.zeros(H, T, dv, dtype=odt, device=dev)
+        o = _new(q, (H, T, dv), odt, stream, zero=True)
     _check("o", o, (H, T, dv), odt, dev)
     if opts is None:
         st = lib.gdn_chunk_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(o), _ptr(s0),
@@ -331,7 +351,7 @@ def gdn_decode_step(q, k, v, beta, g, state, o=None, scale: float = 1.0, stream=
     _check("state", state, (N, H, dk, dv), torch.float32, dev)
     odt, opts = _out_opts(o, out_dtype, d_skip, H, dv, dev, vec, xnorm, xnorm_weight, xnorm_eps)
     if o is None:
-        o = torch.empty(N, H, dv, dtype=odt, device=dev)
+        o = _new(q, (N, H, dv), odt, stream)
     _check("o", o, (N, H, dv), odt, dev)
     if opts is None:
         st = lib.gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(state),
@@ -380,11 +400,11 @@ def gdn_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: int = 64
     _check("ds_final", ds_final, (B, H, dk, dv), torch.float32, dev, required=False)
     need = gdn_chunk_bwd_workspace_bytes(B, H, L, dk, dv, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    out = {"dq": torch.empty(B, H, L, dk, **f32), "dk": torch.empty(B, H, L, dk, **f32),
-           "dv": torch.empty(B, H, L, dv, **f32), "dbeta": None if beta is None else torch.empty(B, H, L, **f32),
-           "dg": None if g is None else torch.empty(B, H, L, **f32), "ds0": torch.empty(B, H, dk, dv, **f32)}
+        workspace = _new(q, max(need, 16), torch.uint8, stream, result=False)
+    new = lambda *shape: _new(q, shape, torch.float32, stream)  # noqa: E731
+    out = {"dq": new(B, H, L, dk), "dk": new(B, H, L, dk), "dv": new(B, H, L, dv),
+           "dbeta": None if beta is None else new(B, H, L), "dg": None if g is None else new(B, H, L),
+           "ds0": new(B, H, dk, dv)}
     st = lib.gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(s0), _ptr(d_o), _ptr(ds_final),
                            _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dbeta"]), _ptr(out["dg"]),
                            _ptr(out["ds0"]), _ptr(workspace), workspace.numel() * workspace.element_size(), B, H, L,

@@ -24,7 +24,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import _check, _out_opts, _raise, lib
+from ._lib import _check, _new, _out_opts, _raise, lib
 
 _BLOCK_SIZES = (16, 32, 64, 128)
 
@@ -43,24 +43,6 @@ def _stream_of(dev: torch.device, stream) -> int:
     if stream is None:
         return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream, result: bool = True) -> torch.Tensor:
-    """A tensor made on the stream that the call uses: what torch hands out on another one may be memory that work queued
-    there still reads or writes. A result made on a passed stream is read on the current one (by a caller who waits),
-    so it is kept until that is through with it too."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    dev = like.device
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(stream)      # (0 is the default stream, which ExternalStream does not take)
-        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-    here = torch.cuda.current_stream(dev)
-    with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    if result and here != stream:
-        t.record_stream(here)
-    return t
 
 
 def _call(f, fn: str, dev: torch.device, args) -> None:
