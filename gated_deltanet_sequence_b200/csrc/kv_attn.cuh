@@ -34,6 +34,35 @@ struct AttnArgs {
 // A 2-D TMA map over the cache as (rows, d) bytes; boxes of box_rows whole rows, swizzled over their width.
 bool make_cache_map(CUtensorMap *m, const void *ptr, long long rows, int d, int box_rows);
 
+// A box of such a map, to shared memory.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+// four e4m3 codes -> two fp16 pairs (exact)
+__device__ __forceinline__ void e4m3_to_h2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+// four values -> four e4m3 codes, nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t e4m3x4(const float (&y)[4]) {
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y[1]), "f"(y[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y[3]), "f"(y[2]));
+    return a | (static_cast<uint32_t>(b) << 16);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Floats of one partial: m and l of 16 rows, then their O.
 __host__ __device__ constexpr long long part_floats(int d) { return 32 + 16ll * d; }
 

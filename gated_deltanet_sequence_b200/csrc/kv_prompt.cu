@@ -102,12 +102,6 @@ template <int D> __device__ __forceinline__ uint64_t kdesc(uint32_t addr) {
 template <int D> __device__ __forceinline__ uint32_t kswz(uint32_t r, uint32_t c) {
     return D == 128 ? sw128(r, c) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
     uint32_t u[32];
     asm volatile(
@@ -156,25 +150,9 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t e4m3x4(const float (&y)[4]) {
-    uint16_t a, b;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y[1]), "f"(y[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y[3]), "f"(y[2]));
-    return a | (static_cast<uint32_t>(b) << 16);
-}
 __device__ __forceinline__ void e4m3_to_h2(uint32_t w, __half2 &lo, __half2 &hi) {
     uint32_t a, b;
-    asm("{\n\t.reg .b16 x, y;\n\t"
-        "mov.b32 {x, y}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, x;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(w));
+    gdn::e4m3_to_h2(w, a, b);
     lo = *reinterpret_cast<const __half2 *>(&a);
     hi = *reinterpret_cast<const __half2 *>(&b);
 }
@@ -342,7 +320,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&bars[full + sl], __popc(boxes) * a.bs * D);
             __syncwarp();
-            if (box) tma_2d(ring + sl * L::kTile8 + 16 * lane * D, map, &bars[full + sl], 0, row);
+            if (box) tma_load_2d(ring + sl * L::kTile8 + 16 * lane * D, map, &bars[full + sl], 0, row);
             if (is_k) {
                 if (lane < 8) s_ks[(j % kKsSlots) * 8 + lane] = ks;
                 if (lane == 0) s_have[j % kKsSlots] = have;
