@@ -216,7 +216,7 @@ struct Worker {
     }
 
     // One step: 32 tokens from position t0. sk, sv: shared addresses of the codes; ks, vs: scales of the step's halves;
-    // edge: some row does not see some token; tok: tokens that exist (bit i: t0 + i).
+    // edge: some row does not see some token; tok: tokens that exist and some row sees (bit i: t0 + i).
     __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, int t0, const float (&ks)[HV], const float (&vs)[HV],
                                          uint32_t tok, bool edge) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -581,10 +581,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         w.saw_nan = false;
 
         const int lo_last = a.window > 0 ? max(p_last, -1) - a.window + 1 : 0;
+        const int lo_first = a.window > 0 ? max(0, max(p_first, -1) - a.window + 1) : 0;      // no row sees a position before it
         struct Step {
             int t;
             float ks[HV], vs[HV];
-            uint32_t tok;          // tokens that exist
+            uint32_t tok;          // tokens that exist and some row sees
             bool edge;             // some row does not see some token
         };
         auto look = [&](int i) {
@@ -601,6 +602,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
                 if (id >= 0) x.tok |= (HV == 1 ? 0xffffffffu : 0xffffu) << (16 * b);
             }
             if (t_hi - x.t < kStep) x.tok &= (1u << (t_hi - x.t)) - 1u;
+            if (x.t < lo_first) x.tok = lo_first - x.t < kStep ? x.tok & (0xffffffffu << (lo_first - x.t)) : 0u;
+            if (HV == 2) {         // a half with nothing to see leaves V's unit alone
+                if ((x.tok & 0xffffu) == 0u) x.vs[0] = x.vs[HV - 1];
+                else if ((x.tok >> 16) == 0u) x.vs[HV - 1] = x.vs[0];
+            }
             x.edge = x.tok != 0xffffffffu || x.t + kStep - 1 > p_first || x.t < lo_last;
             return x;
         };

@@ -469,11 +469,11 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  within 2^-17.8 of that element below). The weights enter as two fp16 parts with an fp32
  *  output (within 2^-23 of themselves or 2^-44 of the row's largest weight), and as one with a
  *  bf16 output (within 2^-12 of themselves or 2^-32 of the largest; 2^-25 in the many-rows
- *  kernel). V scales of a request's blocks may be any powers of two apart; from 2^64 below the
- *  largest on, a block's weights carry what is missing (and are lost below those bounds). A
- *  position that a query does not see does not reach its result, whatever its values; a NaN
- *  that it sees (append stores infinities as NaN) makes its result NaN, a NaN of V in that
- *  column alone. Infinite queries give NaN.
+ *  kernel). V scales of a request's blocks may be any powers of two apart; what lies more than
+ *  2^64 below the largest |V| that some row of the request sees is within 2^-90 of that |V|
+ *  for each token. A position that a query does not see reaches its result in no other way,
+ *  whatever its values; a NaN that it sees (append stores infinities as NaN) makes its result
+ *  NaN, a NaN of V in that column alone. Infinite queries give NaN.
  *  Requests of more than 64 rows (query tokens x query heads of a KV head) run on a tcgen05
  *  kernel when q and o are bf16 and the batch may hold prompts of thousands of rows: (T - N + 1)
  *  * Hq of 40 (d = 128) or 58 (d = 64) rows for each SM, max_q_len * Hq / Hkv above 64. All

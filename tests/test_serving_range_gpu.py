@@ -313,3 +313,18 @@ def test_attn_over_the_longest_context(S, lib):
         assert lib.gdn_sync_status() == 0
         assert (o - one[0]).abs().max() <= 2.0 ** -7 * one[0].abs().max()
         assert (lse - one[1] - math.log(n // bs)).abs().max() <= 2.0 ** -7
+
+
+@pytest.mark.parametrize("bs,d,dtype,out", [(16, 64, torch.float32, torch.float32), (16, 128, torch.bfloat16, torch.bfloat16),
+                                            (64, 128, torch.bfloat16, torch.float32), (32, 64, torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("window", [1, 9, 40, 200])
+def test_attn_blocks_before_the_window_do_not_set_the_unit(S, lib, bs, d, dtype, out, window):
+    """Blocks that no row sees hold values 2^150 larger than those in the window, in every place that a window's start
+    can have in a step: the result is as exact as without them."""
+    for n in (431, 432, 440, 448, 449, 463, 511, 512):
+        cache, q, table, tab, cu = unit_case(S, [-70], n, 1, 4, d, bs, dtype, seed=n)
+        first = max(0, n - window) // bs
+        for i, b in enumerate(table[0]):
+            if i < first:
+                cache.v_scale[b] = 2.0 ** 80
+        attn_check(S, lib, cache, q, table, tab, cu, [n], window, 0.02, out)
