@@ -13,8 +13,8 @@
 // the next token's operands are fetched before the first of them, so that a drafted run of
 // tokens does not wait for memory at each. Every block looks through the slots before its own
 // request's, so that a slot named twice is found on the device and no two blocks update one state.
-// One token of 256 requests, 32 heads of 128 x 128 (1.08 GB): 180 us, 6.0 TB/s; up to six tokens of 48
-// requests, 16 heads of 64 x 128 (40 MB): 15.5 us.
+// One token of 256 requests, 32 heads of 128 x 128 (1.08 GB): 173 us, 6.2 TB/s; up to six tokens of 48
+// requests, 16 heads of 64 x 128 (40 MB): 16.2 us.
 #include "common.cuh"
 #include "tc_kernels.cuh"
 

@@ -12,7 +12,7 @@
 // the codes. A block of 256 threads looks over R rows and takes the runs that start there: runs
 // that a warp holds in a few registers (decode: one row) go one to a warp, longer ones (prompts)
 // to the whole block. DRAM bytes bound it: rows in, codes out. 24 prompts of 157 to 4096 rows, 16 heads, d =
-// 128 (386 MB): 85 us, 4.5 TB/s; a run's codes wait for its maximum, so a block's next run is loaded
+// 128 (386 MB): 82 us, 4.7 TB/s; a run's codes wait for its maximum, so a block's next run is loaded
 // meanwhile (without that, and one head a block, 186 us).
 #include "common.cuh"
 #include "tc_kernels.cuh"

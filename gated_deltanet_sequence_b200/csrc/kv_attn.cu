@@ -27,7 +27,7 @@
 // eight lanes of a quarter-warp hit different banks.
 //
 // Measured (one B200): 64 requests of 128 to 16384 tokens, 32 query and 8 KV heads, d = 128, 441 MB:
-// 106 us (4.2 TB/s); a block's loop alone moves 5.7 TB/s, the rest is units' starts and ends (8 thousand
+// 105 us (4.2 TB/s); a block's loop alone moves 5.7 TB/s, the rest is units' starts and ends (8 thousand
 // cycles each) and blocks that end apart. Warp-level MMA is enough here: with K's codes as an operand
 // the tensor pipe is 40 % busy. Two blocks an SM (255 registers) hold 128 KB of copies in flight, and
 // three stages a warp reached the rate of a plain copy loop; more and smaller shares (two a block) were

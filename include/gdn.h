@@ -453,7 +453,8 @@ gdn_status_t gdn_kv_append(const void *k, const void *v, long long k_stride, lon
  *  q            (T, Hq, d) in_dtype, rows q_stride elements apart                     read
  *  block_table  (N, max_blocks) int32; entries of positions < kv_lens[n] are read     read
  *  cu_seqlens   (N + 1) int32, kv_lens (N) int32                                      read
- *  o            (T, Hq, d) out_dtype                                               written
+ *  o            (T, Hq, d) out_dtype; o, lse and the workspace overlap nothing that is read
+ *                                                                                  written
  *  lse          (T, Hq) fp32, nullable                                             written
  *  max_q_len    an upper bound of the rows of one request, >= 1: it chooses between the forms
  *               for few and for many rows; a request with more rows than it says is left out
