@@ -408,8 +408,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         auto scale_of = [&](int id) {
             return id >= 0 && id < a.num_blocks ? a.v_scale[static_cast<long long>(id) * a.Hkv + h] : -1.f;
         };
-        // V's largest scale here is the unit that V is converted in; the smallest of a block that is not all zeros has to
-        // be within kSpread of it, or fp16 would lose it
+        // V's largest scale here is the unit that V is converted in; the smallest has to be within kSpread of it, or fp16
+        // would lose its block. A block of zeros has the smallest scale that there is, which says nothing here; whether it is
+        // one is seen when it is converted.
         float vu;
         {
             float mx = kMinScale, mn = __int_as_float(0x7f800000);
@@ -439,7 +440,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const float inv_vu = 1.f / vu;
         float s_next = scale_of(block_of(0));             // negative: the token does not exist
         int id_next = block_of(1);
-        bool ok = true, nan = false;
+        bool ok = true, leave = false;                    // leave: something that fp16 does not hold
         for (int j = 0; j < nt && ok; ++j) {
             const int sl = j % kVStages, csl = j % kCStages;
             const float s_raw = s_next;
@@ -453,6 +454,15 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const __half2 f = __float2half2_rn(s);
             __half2 probe = __float2half2_rn(0.f);
             const uint8_t *src = smem + L::OFF_V8 + sl * L::kTile8;
+            if (e && s < 1.f / kSpread) {                 // the smallest scale: a block of zeros, unless it holds something
+                uint32_t any = 0u;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + kswz<D>(tk, c));
+                    any |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+                }
+                leave |= any != 0u;
+            }
             uint8_t *dst = smem + L::OFF_V + csl * L::kTile16;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -476,7 +486,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 *reinterpret_cast<uint4 *>(half + sw128(tk, (2 * c) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4 *>(half + sw128(tk, (2 * c + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            nan |= __half2float(__low2half(probe)) != 0.f || __half2float(__high2half(probe)) != 0.f;
+            leave |= __half2float(__low2half(probe)) != 0.f || __half2float(__high2half(probe)) != 0.f;
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -484,7 +494,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 mbar_arrive(&bars[B_VE + sl]);
             }
         }
-        if (nan) redo[u.n] = 1;
+        if (leave) redo[u.n] = 1;
     } else if (warp >= 8) {
         // ================================================================ a group's rows, one a thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");

@@ -328,3 +328,18 @@ def test_attn_blocks_before_the_window_do_not_set_the_unit(S, lib, bs, d, dtype,
             if i < first:
                 cache.v_scale[b] = 2.0 ** 80
         attn_check(S, lib, cache, q, table, tab, cu, [n], window, 0.02, out)
+
+
+@pytest.mark.parametrize("pad", [0, 9000])
+@pytest.mark.parametrize("big,codes", [(-60, True), (-84, True), (-90, True), (-60, False)])
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 64)])
+def test_attn_prompt_values_at_the_smallest_scale(S, lib, d, bs, big, codes, pad):
+    """Blocks of append's smallest scale, 2^-100, that are not zeros, beside blocks of larger values: rows that see them
+    alone have them in full. (Blocks of zeros there do not matter.)"""
+    n = 300
+    cache, q, table, tab, cu = unit_case(S, [big], n, 2, 2, d, bs, torch.bfloat16, seed=43, ql=n)
+    for b in table[0][:64 // bs]:                        # the first 64 tokens: half of a unit of the many-rows kernel
+        cache.v_scale[b] = 2.0 ** -100
+        if not codes:
+            cache.v.view(torch.uint8)[b] = 0
+    attn_check(S, lib, cache, q, table, tab, cu, [n], 0, 0.02, torch.bfloat16, pad=pad)
