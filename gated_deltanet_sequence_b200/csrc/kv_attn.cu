@@ -410,8 +410,8 @@ struct Worker {
                             mma16816(acc, p[k], b0, b1);
                         }
                     }
-                    // (blocks of 16 tokens, twice as many of these sums: two-wide, 146 against 151 us for fp32 queries, 64 requests;
-                    // with one sum a step the pairs cost more moves than they save, 118 against 115 us before the step's sum)
+                    // (blocks of 16 tokens have twice as many of these sums: two-wide, 64 requests of fp32 queries 146 us against
+                    // 151; with larger blocks that was slower, 118 us against 115 for bf16 queries)
                     if constexpr (PSPLIT && HV == 2) {
 #pragma unroll
                         for (int r = 0; r < 4; r += 2) add_parts(acc[r], acc[r + 1], t[r], t[r + 1], tl[r], tl[r + 1]);

@@ -67,6 +67,44 @@ def test_the_default_stream_by_its_handle(S, lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and lib.gdn_sync_status() == 0
 
 
+def test_calls_on_a_forked_stream_are_captured(S, lib):
+    """A graph whose capture forks: attention and recurrence side by side on two streams, results and workspaces made in
+    the calls, replayed with other inputs."""
+    kv, ql = [900, 70, 2000], [1, 2, 1]
+    cache, q, table, tab, cu = attn_case(S, kv, ql, 2, 4, 128, 64, torch.bfloat16, seed=18)
+    cu_t, kv_t = i32(cu), i32(kv)
+    gq, gk, gv, beta, g, state = slots_inputs(4, 2, 4, 64, 64, 3, torch.bfloat16, seed=19)
+    slots, start = i32([2, 0, 1]), state.clone()
+
+    def both(side):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        o, lse = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, max_q_len=2, scale=0.09, lse=True, stream=side)
+        r = S.gdn_decode_slots(gq, gk, gv, beta, g, state, slots, cu_t)
+        p, _ = S.gdn_kv_attn(cache, q, tab, cu_t, kv_t, max_q_len=2, scale=0.05)
+        here.wait_stream(side)
+        return o, lse, r, p
+
+    side = torch.cuda.Stream()
+    both(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(side)
+    for turn in range(3):
+        q.copy_(torch.randn(q.shape, generator=_gen(turn), device=DEV))
+        state.copy_(start)
+        for x in got:
+            x.fill_(5.0)
+        graph.replay()
+        after = state.clone()
+        state.copy_(start)
+        want = both(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(after, state), turn
+    assert lib.gdn_sync_status() == 0
+
+
 # ---------------------------------------------------------------- V's block scales
 def unit_case(S, scales, n, Hkv, G, d, bs, dtype, seed, positive=True, ql=1):
     """One request of n tokens whose blocks' V scales go through `scales` in turn (a block of zeros where that is None),
